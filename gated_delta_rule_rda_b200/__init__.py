@@ -15,8 +15,15 @@ Functions mirror the C entry points of ``include/rda.h``:
 - :func:`rda_prep_inputs`, :func:`rda_output_gate_norm` -- the steps either side of
   the core (short convolutions, q/k norms, gates; output RMSNorm times the gate);
 - :func:`rda_backward` -- the gradients of the core;
+- :func:`rda_latent_prefill`, :func:`rda_latent_backward` -- the hybrid's other layers:
+  attention with a key part shared by the heads, over packed sequences, and its gradients;
+- :func:`rda_latent_decode` -- the same attention in its absorbed form, 1..8 tokens per
+  sequence over a paged cache of one latent vector per token;
+- :func:`rda_verify_drafts` -- which drafted tokens stay, and the next one, from given
+  random numbers;
 - :func:`rda_read_device_error`, :func:`rda_prefill_workspace_bytes`,
-  :func:`rda_prefill_channel_workspace_bytes`.
+  :func:`rda_prefill_channel_workspace_bytes`, and the ``*_workspace_bytes`` of the
+  latent-attention and verification calls.
 
 The raw ctypes handle is :data:`lib` (``lib.rda_prefill_chunked(...)`` takes
 plain pointers and sizes, including host-pointer use for the varlen schedule).
@@ -76,6 +83,22 @@ lib.rda_backward_workspace_bytes.argtypes = [_i] * 5
 lib.rda_backward_workspace_bytes.restype = _sz
 lib.rda_backward.argtypes = [_vp] * 16 + [_i] * 6 + [_f, _vp, _sz, _vp]
 lib.rda_backward.restype = _i
+lib.rda_latent_prefill_workspace_bytes.argtypes = [_i] * 7
+lib.rda_latent_prefill_workspace_bytes.restype = _sz
+lib.rda_latent_prefill.argtypes = [_vp] * 7 + [_i] * 3 + [_vp] * 2 + [_i] * 5 + [_f, _i, _vp, _sz, _vp]
+lib.rda_latent_prefill.restype = _i
+lib.rda_latent_backward_workspace_bytes.argtypes = [_i] * 7
+lib.rda_latent_backward_workspace_bytes.restype = _sz
+lib.rda_latent_backward.argtypes = [_vp] * 10 + [_i] * 3 + [_vp] * 5 + [_i] * 5 + [_f, _i, _vp, _sz, _vp]
+lib.rda_latent_backward.restype = _i
+lib.rda_latent_decode_workspace_bytes.argtypes = [_i] * 5
+lib.rda_latent_decode_workspace_bytes.restype = _sz
+lib.rda_latent_decode.argtypes = [_vp] * 7 + [_i] * 9 + [_f, _vp, _sz, _vp]
+lib.rda_latent_decode.restype = _i
+lib.rda_verify_drafts_workspace_bytes.argtypes = [_i] * 3
+lib.rda_verify_drafts_workspace_bytes.restype = _sz
+lib.rda_verify_drafts.argtypes = [_vp] * 7 + [_i] * 3 + [_vp, _sz, _vp]
+lib.rda_verify_drafts.restype = _i
 lib.rda_debug_set_wait_fault.argtypes = [_i, ctypes.c_ulonglong]
 lib.rda_debug_set_wait_fault.restype = None
 
@@ -383,6 +406,208 @@ def rda_backward(q, k, v, log_alpha, beta, d_out, write_gate=None, initial_state
     return g
 
 
+def rda_latent_prefill_workspace_bytes(total_q, total_k, H, Dk, Ds, Dv, num_seqs) -> int:
+    return int(lib.rda_latent_prefill_workspace_bytes(total_q, total_k, H, Dk, Ds, Dv, num_seqs))
+
+
+def rda_latent_backward_workspace_bytes(total_q, total_k, H, Dk, Ds, Dv, num_seqs) -> int:
+    return int(lib.rda_latent_backward_workspace_bytes(total_q, total_k, H, Dk, Ds, Dv, num_seqs))
+
+
+def rda_latent_decode_workspace_bytes(B, T, H, Dl, Ds) -> int:
+    return int(lib.rda_latent_decode_workspace_bytes(B, T, H, Dl, Ds))
+
+
+def rda_verify_drafts_workspace_bytes(B, T, V) -> int:
+    return int(lib.rda_verify_drafts_workspace_bytes(B, T, V))
+
+
+def _need_like(t, name, shape, dtype, device):
+    """A contiguous CUDA tensor of this shape and type on this device."""
+    if not t.is_cuda:
+        raise ValueError("rda: tensors must be CUDA tensors (no CPU path exists)")
+    if t.device != device:
+        raise ValueError(f"rda: {name} is on {t.device}, other tensors on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"rda: {name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"rda: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"rda: {name} must be contiguous")
+
+
+def _launch(fn, device, stream, *args):
+    """Calls a library function on ``device`` (its current stream unless one is
+    given), whatever device is current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"rda: the stream belongs to {stream.device}, the tensors to {device}")
+    s = ctypes.c_void_p(stream.cuda_stream)
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, s)
+    _check(code, fn.__name__)
+
+
+def _latent_sizes(q, k, v, q_shared, k_shared, cu_q, cu_k):
+    """Checks the inputs of the expanded form; returns (total_q, total_k, H, Dk, Ds, Dv, N)."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("rda: q, k and v are [total, H, D], cu_seqlens [N + 1]")
+    if (q_shared is None) != (k_shared is None):
+        raise ValueError("rda: q_shared and k_shared come together")
+    total_q, H, Dk = q.shape
+    total_k, Dv = k.shape[0], v.shape[2]
+    Ds = 0 if k_shared is None else k_shared.shape[-1]
+    dev, dt = q.device, q.dtype
+    _dtype_code(q)
+    _need_like(q, "q", (total_q, H, Dk), dt, dev)
+    _need_like(k, "k", (total_k, H, Dk), dt, dev)
+    _need_like(v, "v", (total_k, H, Dv), dt, dev)
+    if Ds:
+        _need_like(q_shared, "q_shared", (total_q, H, Ds), dt, dev)
+        _need_like(k_shared, "k_shared", (total_k, Ds), dt, dev)
+    elif k_shared is not None:
+        raise ValueError("rda: pass no shared parts rather than empty ones")
+    N = cu_q.numel() - 1
+    _need_like(cu_q, "cu_seqlens_q", (N + 1,), torch.int32, dev)
+    _need_like(cu_k, "cu_seqlens_k", (N + 1,), torch.int32, dev)
+    return total_q, total_k, H, Dk, Ds, Dv, N
+
+
+def rda_latent_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, scale, q_shared=None, k_shared=None,
+                       causal=True, out=None, lse=None, return_lse=False, workspace=None, stream=None):
+    """Latent attention in its expanded form over packed sequences: scores
+    ``scale * (q . k + q_shared . k_shared)``, softmax over the keys a query sees.
+
+    q ``[total_q,H,Dk]``, k ``[total_k,H,Dk]``, v ``[total_k,H,Dv]`` (per head, from the latents);
+    q_shared ``[total_q,H,Ds]`` and k_shared ``[total_k,Ds]`` (one key part for all heads), or
+    neither; cu_seqlens int32 CUDA ``[N+1]`` (``cu_seqlens_k`` None: the queries').  ``causal``
+    aligns a sequence's last query with its last key.  Returns ``(out [total_q,H,Dv], lse fp32
+    [total_q,H] or None)``; a query that sees no key gives zeros and -inf.  Rows behind the last
+    sequence are not written.
+    """
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    total_q, total_k, H, Dk, Ds, Dv, N = sizes = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
+    dev = q.device
+    if out is None:
+        out = torch.empty((total_q, H, Dv), dtype=q.dtype, device=dev)
+    else:
+        _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
+    if lse is not None:
+        _need_like(lse, "lse", (total_q, H), torch.float32, dev)
+    elif return_lse:
+        lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = new_workspace(rda_latent_prefill_workspace_bytes(*sizes), dev)
+    _launch(lib.rda_latent_prefill, dev, stream, _ptr(q), _ptr(q_shared), _ptr(k), _ptr(k_shared), _ptr(v),
+            _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), N, total_q, total_k, _ptr(out), _ptr(lse), _dtype_code(q),
+            H, Dk, Ds, Dv, float(scale), int(bool(causal)), _ptr(workspace), workspace.numel())
+    return out, lse
+
+
+def rda_latent_backward(q, k, v, out, lse, d_out, cu_seqlens_q, cu_seqlens_k=None, *, scale, q_shared=None,
+                        k_shared=None, causal=True, workspace=None, stream=None):
+    """Gradients of ``<d_out, out>`` for :func:`rda_latent_prefill`, from its inputs, its
+    ``out`` and its ``lse``.  Returns a dict of tensors like the inputs (their dtype): dq, dk, dv,
+    dq_shared and dk_shared (None without shared parts; dk_shared is summed over the heads).
+    Rows behind the last sequence are not written.  Deterministic."""
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    total_q, total_k, H, Dk, Ds, Dv, N = sizes = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
+    dev = q.device
+    _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
+    _need_like(d_out, "d_out", (total_q, H, Dv), q.dtype, dev)
+    _need_like(lse, "lse", (total_q, H), torch.float32, dev)
+    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+             dq_shared=torch.empty_like(q_shared) if Ds else None,
+             dk_shared=torch.empty_like(k_shared) if Ds else None)
+    if workspace is None:
+        workspace = new_workspace(rda_latent_backward_workspace_bytes(*sizes), dev)
+    _launch(lib.rda_latent_backward, dev, stream, _ptr(q), _ptr(q_shared), _ptr(k), _ptr(k_shared), _ptr(v),
+            _ptr(out), _ptr(lse), _ptr(d_out), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), N, total_q, total_k,
+            _ptr(g["dq"]), _ptr(g["dq_shared"]), _ptr(g["dk"]), _ptr(g["dk_shared"]), _ptr(g["dv"]),
+            _dtype_code(q), H, Dk, Ds, Dv, float(scale), int(bool(causal)), _ptr(workspace), workspace.numel())
+    return g
+
+
+def rda_latent_decode(q, pages, block_table, seq_lens, *, scale, q_shared=None, out=None, lse=None,
+                      return_lse=False, workspace=None, stream=None):
+    """Latent attention in its absorbed form over a paged cache, 1..8 new tokens per sequence.
+
+    q ``[B,T,H,Dl]`` (queries taken into the latent space), q_shared ``[B,T,H,Ds]`` or None;
+    pages ``[num_pages,page_size,Dl+Ds]`` (a token's latent vector, its shared key part behind it);
+    block_table int32 ``[B,W]``: the pages of each sequence in order; seq_lens int32 ``[B]``: cached
+    tokens, the T new ones among them.  Query t sees the first ``seq_lens - T + t + 1``.
+    Returns ``(out [B,T,H,Dl], lse fp32 [B,T,H] or None)``; the values are the latents."""
+    if q.dim() != 4 or pages.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("rda: q is [B, T, H, Dl], pages [num_pages, page_size, Dl + Ds], block_table [B, W]")
+    B, T, H, Dl = q.shape
+    num_pages, page_size, D = pages.shape
+    Ds = 0 if q_shared is None else q_shared.shape[-1]
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
+    _need_like(q, "q", (B, T, H, Dl), dt, dev)
+    if q_shared is not None:
+        _need_like(q_shared, "q_shared", (B, T, H, Ds), dt, dev)
+    _need_like(pages, "pages", (num_pages, page_size, Dl + Ds), dt, dev)
+    _need_like(block_table, "block_table", (B, block_table.shape[1]), torch.int32, dev)
+    _need_like(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((B, T, H, Dl), dtype=dt, device=dev)
+    else:
+        _need_like(out, "out", (B, T, H, Dl), dt, dev)
+    if lse is not None:
+        _need_like(lse, "lse", (B, T, H), torch.float32, dev)
+    elif return_lse:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = new_workspace(rda_latent_decode_workspace_bytes(B, T, H, Dl, Ds), dev)
+    _launch(lib.rda_latent_decode, dev, stream, _ptr(q), _ptr(q_shared), _ptr(pages), _ptr(block_table),
+            _ptr(seq_lens), _ptr(out), _ptr(lse), code, B, T, H, Dl, Ds, num_pages, page_size,
+            block_table.shape[1], float(scale), _ptr(workspace), workspace.numel())
+    return out, lse
+
+
+def rda_verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, num_drafts=None, tokens=None,
+                      num_accepted=None, workspace=None, stream=None):
+    """Verification of drafted tokens (speculative sampling) from given random numbers.
+
+    draft_tokens int32 ``[B,T]``; target_probs fp32 ``[B,T+1,V]``; uniforms fp32 ``[B,T+1]`` in [0, 1);
+    draft_probs fp32 ``[B,T,V]``, or None for drafts chosen outright; num_drafts int32 ``[B]`` or
+    None (all T).  Returns ``(tokens int32 [B,T+1], num_accepted int32 [B])``: the accepted drafts,
+    the token drawn after them, then -1."""
+    if draft_tokens.dim() != 2 or target_probs.dim() != 3:
+        raise ValueError("rda: draft_tokens is [B, T], target_probs [B, T + 1, V]")
+    B, T = draft_tokens.shape
+    V = target_probs.shape[2]
+    dev = target_probs.device
+    _need_like(draft_tokens, "draft_tokens", (B, T), torch.int32, dev)
+    _need_like(target_probs, "target_probs", (B, T + 1, V), torch.float32, dev)
+    _need_like(uniforms, "uniforms", (B, T + 1), torch.float32, dev)
+    if draft_probs is not None:
+        _need_like(draft_probs, "draft_probs", (B, T, V), torch.float32, dev)
+    if num_drafts is not None:
+        _need_like(num_drafts, "num_drafts", (B,), torch.int32, dev)
+    if tokens is None:
+        tokens = torch.empty((B, T + 1), dtype=torch.int32, device=dev)
+    else:
+        _need_like(tokens, "tokens", (B, T + 1), torch.int32, dev)
+    if num_accepted is None:
+        num_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+    else:
+        _need_like(num_accepted, "num_accepted", (B,), torch.int32, dev)
+    if workspace is None:
+        workspace = new_workspace(rda_verify_drafts_workspace_bytes(B, T, V), dev)
+    _launch(lib.rda_verify_drafts, dev, stream, _ptr(draft_tokens), _ptr(draft_probs), _ptr(target_probs),
+            _ptr(uniforms), _ptr(num_drafts), _ptr(tokens), _ptr(num_accepted), B, T, V, _ptr(workspace),
+            workspace.numel())
+    return tokens, num_accepted
+
+
 def rda_debug_set_wait_fault(drop_chunk=-1, wait_limit_ns=0):
     """Testing only: bound of the device-side waits and an injected stall of the
     scan (see include/rda.h); ``rda_debug_set_wait_fault()`` turns it off."""
@@ -399,6 +624,9 @@ def rda_read_device_error(workspace, stream=None) -> int:
 __all__ = ["rda_prefill_chunked", "rda_prefill_varlen", "rda_decode_step", "rda_decode_tokens",
            "rda_prep_inputs", "rda_output_gate_norm", "rda_backward",
            "rda_prefill_chunked_noalloc",
+           "rda_latent_prefill", "rda_latent_backward", "rda_latent_decode", "rda_verify_drafts",
+           "rda_latent_prefill_workspace_bytes", "rda_latent_backward_workspace_bytes",
+           "rda_latent_decode_workspace_bytes", "rda_verify_drafts_workspace_bytes",
            "rda_read_device_error", "rda_debug_set_wait_fault", "rda_prefill_workspace_bytes",
            "rda_prefill_channel_workspace_bytes", "new_workspace", "version",
            "RdaError", "lib", "LIB_PATH"]

@@ -1,0 +1,112 @@
+// Launch interface of the latent-attention kernels and of draft verification.
+// Not installed; the public interface is include/rda.h.
+#pragma once
+
+#include <atomic>
+
+#include "rda_internal.h"
+
+namespace rda {
+
+// Lets kernel K have `bytes` of dynamic shared memory, once per device (the
+// attribute belongs to the device's copy of the kernel).
+template <auto K> cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+// Arguments of the expanded form (packed sequences) and of its gradients.
+struct LatentArgs {
+    const void *q, *q_shared, *k, *k_shared, *v;   // q_shared, k_shared: null exactly when Ds = 0
+    const int32_t *cu_q, *cu_k;
+    int num_seqs, total_q, total_k;
+    int H, Dk, Ds, Dv;
+    float scale;
+    int causal;
+    rda_dtype_t dtype;
+    void *out;                   // forward: written; backward: read
+    float *lse;                  // forward: written (or null); backward: read
+    int32_t *err;                // device error word
+    uint64_t wait_ns;            // bound of every device-side wait
+    // backward only
+    const void *d_out;
+    void *dq, *dq_shared, *dk, *dk_shared, *dv;
+    float *delta;                // workspace: sum_d d_out out, [total_q, H]
+    float *dks_heads;            // workspace: the shared key part's gradient per head, [total_k, H, Ds]
+};
+
+// Arguments of the absorbed form over a paged cache.
+struct LatentDecodeArgs {
+    const void *q, *q_shared, *pages;
+    const int32_t *table, *lens;
+    int num_pages, page_size, table_width;
+    int B, T, H, Dl, Ds;
+    float scale;
+    rda_dtype_t dtype;
+    void *out;
+    float *lse;
+    int32_t *err;
+    uint64_t wait_ns;
+    float *part;                 // workspace: partial outputs and their log-sum-exps
+};
+
+struct VerifyArgs {
+    const int32_t *draft;        // [B, T]
+    const float *draft_probs;    // [B, T, V] or null
+    const float *target_probs;   // [B, T + 1, V]
+    const float *uniforms;       // [B, T + 1]
+    const int32_t *num_drafts;   // [B] or null
+    int32_t *tokens, *num_accepted;
+    int B, T, V;
+    double2 *part;               // workspace: sums of the weights per slice
+};
+
+// Most drafted tokens one verification takes per sequence (one warp lane each).
+constexpr int kMaxDrafts = 32;
+
+// Tokens of sequence n in a packed batch, with whatever the device array holds
+// kept inside [0, total].
+struct SeqSpan {
+    int start, len;
+};
+__device__ __forceinline__ int clamped(const int32_t *cu, int n, int total) { return min(max(cu[n], 0), total); }
+__device__ __forceinline__ SeqSpan seq_span(const int32_t *cu, int n, int total) {
+    const int s = clamped(cu, n, total);
+    return SeqSpan{s, max(clamped(cu, n + 1, total) - s, 0)};
+}
+// Tiles of `tile` rows over packed sequences without a prefix sum: sequence n
+// owns the slots from floor(cu[n] / tile) + n on, which are as many as its
+// rows need or one more, since ceil(len / tile) <= floor((c + len) / tile) -
+// floor(c / tile) + 1.  Returns the sequence that owns `slot` and the tile in it.
+__device__ __forceinline__ int find_tile(const int32_t *cu, int num_seqs, int total, int tile, int slot, int *t) {
+    int lo = 0, hi = num_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (clamped(cu, mid, total) / tile + mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    *t = slot - (clamped(cu, lo, total) / tile + lo);
+    return lo;
+}
+inline int tile_slots(int total, int num_seqs, int tile) { return total / tile + num_seqs; }
+
+cudaError_t launch_latent_forward_f32(const LatentArgs &a, cudaStream_t s);
+cudaError_t launch_latent_backward_f32(const LatentArgs &a, cudaStream_t s);
+// shared steps of the gradients: delta before, the sum over heads after
+cudaError_t launch_latent_delta(const LatentArgs &a, cudaStream_t s);
+cudaError_t launch_latent_shared_sum(const LatentArgs &a, cudaStream_t s);
+cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s);
+cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s);
+
+size_t latent_backward_scratch_bytes(int total_q, int total_k, int H, int Ds);
+size_t latent_decode_scratch_bytes(int B, int T, int H, int Dl);
+size_t verify_scratch_bytes(int B, int V);
+
+}  // namespace rda

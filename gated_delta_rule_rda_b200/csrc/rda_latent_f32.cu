@@ -1,0 +1,636 @@
+// Latent attention on the fp32 pipes: the expanded form (forward and
+// gradients) and the absorbed form over a paged cache.
+//
+//   s_ij = scale (q_i . k_j + q~_i . k~_j),  p = softmax_j s,  o_i = sum_j p_ij v_j
+//   ds_ij = p_ij (do_i . v_j - do_i . o_i),  dq = scale ds k,  dk = scale ds^T q,  dv = p^T do
+//
+// fp32 inputs are held to fp32 accuracy, which tensor-core operands of 16 or
+// 19 bits do not give, so these kernels run on FMAs: register tiles of 4 x 4
+// scores and 4 x (D / 16) outputs a thread, operands as fp32 rows in shared
+// memory (a row stride of D + 4 floats keeps the 128-bit reads of eight
+// consecutive rows on different banks).
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "rda_io.cuh"
+#include "rda_latent.h"
+
+namespace rda {
+namespace {
+
+constexpr int kTile = 64;         // query rows and keys per tile
+constexpr int kThreads = 256;
+constexpr int kLdP = kTile + 4;
+
+// Rows [row0, row0 + n) of head h as fp32 into dst[64][ld]: `part` ([rows, H, D0])
+// and behind it `shared` ([rows, Hs, D1], the same for every head if Hs = 1).
+// Rows from n on are zero, whatever lies behind a sequence.
+template <typename T>
+__device__ __forceinline__ void load_rows(float *dst, int ld, const T *part, int D0, const T *shared, int D1, int Hs,
+                                          long row0, int n, int H, int h) {
+    const int per = (D0 + D1) / 4;
+    for (int e = threadIdx.x; e < kTile * per; e += kThreads) {
+        const int r = e / per, c = (e % per) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n) {
+            const size_t row = (size_t)(row0 + r);
+            x = c < D0 ? Io<T>::ld4(part + (row * H + h) * D0 + c)
+                       : Io<T>::ld4(shared + (row * Hs + (Hs == 1 ? 0 : h)) * D1 + (c - D0));
+        }
+        *reinterpret_cast<float4 *>(dst + r * ld + c) = x;
+    }
+}
+
+// acc[i][j] += a[4 ty + i] . b[tx + 16 j] over D
+__device__ __forceinline__ void dot44(float (&acc)[4][4], const float *a, int lda, const float *b, int ldb, int D) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const float *ar = a + 4 * ty * lda, *br = b + tx * ldb;
+#pragma unroll 2
+    for (int d = 0; d < D; d += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = *reinterpret_cast<const float4 *>(ar + i * lda + d);
+            y[i] = *reinterpret_cast<const float4 *>(br + 16 * i * ldb + d);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+    }
+}
+
+// acc[i][4 c ..] += sum_j w[4 ty + i][j] b[j][64 c + 4 tx ..]   (w row-major)
+template <int NC>
+__device__ __forceinline__ void rows_times(float (&acc)[4][NC][4], const float *w, const float *b, int ldb) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 1
+    for (int j = 0; j < kTile; j += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(w + (4 * ty + i) * kLdP + j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const float4 y = *reinterpret_cast<const float4 *>(b + (j + u) * ldb + 64 * c + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = u == 0 ? x[i].x : u == 1 ? x[i].y : u == 2 ? x[i].z : x[i].w;
+                    acc[i][c][0] = fmaf(p, y.x, acc[i][c][0]);
+                    acc[i][c][1] = fmaf(p, y.y, acc[i][c][1]);
+                    acc[i][c][2] = fmaf(p, y.z, acc[i][c][2]);
+                    acc[i][c][3] = fmaf(p, y.w, acc[i][c][3]);
+                }
+            }
+    }
+}
+// acc[i][4 c ..] += sum_r w[r][4 ty + i] b[r][64 c + 4 tx ..]   (the transpose of w)
+template <int NC>
+__device__ __forceinline__ void cols_times(float (&acc)[4][NC][4], const float *w, const float *b, int ldb) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 4
+    for (int r = 0; r < kTile; ++r) {
+        const float4 x = *reinterpret_cast<const float4 *>(w + r * kLdP + 4 * ty);
+        const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const float4 y = *reinterpret_cast<const float4 *>(b + r * ldb + 64 * c + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i][c][0] = fmaf(xs[i], y.x, acc[i][c][0]);
+                acc[i][c][1] = fmaf(xs[i], y.y, acc[i][c][1]);
+                acc[i][c][2] = fmaf(xs[i], y.z, acc[i][c][2]);
+                acc[i][c][3] = fmaf(xs[i], y.w, acc[i][c][3]);
+            }
+        }
+    }
+}
+
+// Columns [64 c, 64 c + 64) of 64 rows to out ([rows, H, D0]) or, from column
+// D0 on, to shared ([rows, H, D1]).
+template <typename T, typename U, int NC>
+__device__ __forceinline__ void store_rows(const float (&acc)[4][NC][4], float f, T *out, int D0, U *shared, int D1,
+                                           long row0, int n, int H, int h) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (4 * ty + i >= n) continue;
+        const size_t row = (size_t)(row0 + 4 * ty + i) * H + h;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int col = 64 * c + 4 * tx;
+            const float4 x = make_float4(f * acc[i][c][0], f * acc[i][c][1], f * acc[i][c][2], f * acc[i][c][3]);
+            if (col < D0) Io<T>::st4(out + row * D0 + col, x);
+            else Io<U>::st4(shared + row * D1 + (col - D0), x);
+        }
+    }
+}
+
+__device__ __forceinline__ bool seen(const LatentArgs &a, int i, int j, int lq, int lk) {
+    return i < lq && j < lk && (!a.causal || j <= i + lk - lq);
+}
+
+// ---------------------------------------------------------------------------
+// Forward: one CTA per (64 query rows, head), online softmax over key tiles.
+// ---------------------------------------------------------------------------
+template <typename T, int NDV>
+__global__ void __launch_bounds__(kThreads) latent_forward_f32_kernel(LatentArgs a) {
+    extern __shared__ __align__(16) float smem[];
+    const int D = a.Dk + a.Ds, ld = D + 4, ldv = 64 * NDV + 4;
+    float *Qs = smem, *Ks = Qs + kTile * ld, *Vs = Ks + kTile * ld, *Ps = Vs + kTile * ldv;
+    int t;
+    // the last tiles of a sequence see the most keys: start with them
+    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, kTile, (int)(gridDim.x - 1 - blockIdx.x), &t);
+    const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
+    const int h = blockIdx.y, r0 = t * kTile;
+    const int rows = min(kTile, sq.len - r0);
+    if (rows <= 0) return;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    load_rows<T>(Qs, ld, (const T *)a.q, a.Dk, (const T *)a.q_shared, a.Ds, a.H, sq.start + r0, rows, a.H, h);
+    float o[4][NDV][4] = {}, m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    const int kend = a.causal ? min(sk.len, r0 + rows + sk.len - sq.len) : sk.len;
+    for (int k0 = 0; k0 < kend; k0 += kTile) {
+        __syncthreads();
+        load_rows<T>(Ks, ld, (const T *)a.k, a.Dk, (const T *)a.k_shared, a.Ds, 1, sk.start + k0,
+                     min(kTile, sk.len - k0), a.H, h);
+        load_rows<T>(Vs, ldv, (const T *)a.v, 64 * NDV, (const T *)nullptr, 0, 1, sk.start + k0,
+                     min(kTile, sk.len - k0), a.H, h);
+        __syncthreads();
+        float s[4][4] = {};
+        dot44(s, Qs, ld, Ks, ld, D);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 4 * ty + i;
+            float top = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = seen(a, r, k0 + tx + 16 * j, sq.len, sk.len) ? s[i][j] * a.scale : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+#pragma unroll
+            for (int off = 8; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float base = top == -INFINITY ? 0.f : top;    // nothing seen so far: every p is e^-inf
+            const float keep = expf(m[i] - base);
+            m[i] = top;
+            l[i] *= keep;
+#pragma unroll
+            for (int c = 0; c < NDV; ++c)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) o[i][c][u] *= keep;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = expf(s[i][j] - base);
+                l[i] += p;
+                Ps[(4 * ty + i) * kLdP + tx + 16 * j] = p;
+            }
+        }
+        __syncthreads();
+        rows_times<NDV>(o, Ps, Vs, ldv);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int off = 8; off; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+        const int r = r0 + 4 * ty + i;
+        if (a.lse && tx == 0 && 4 * ty + i < rows)
+            a.lse[(size_t)(sq.start + r) * a.H + h] = l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
+        const float f = l[i] > 0.f ? 1.f / l[i] : 0.f;
+#pragma unroll
+        for (int c = 0; c < NDV; ++c)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[i][c][u] *= f;
+    }
+    store_rows<T, T, NDV>(o, 1.f, (T *)a.out, 64 * NDV, (T *)nullptr, 0, sq.start + r0, rows, a.H, h);
+}
+
+// ---------------------------------------------------------------------------
+// Gradients.  Two kernels, each with the sums that its CTA owns in registers
+// (keys, or query rows), so that no sum depends on the order of atomics; the
+// price is that the scores and do . v are formed twice.
+// ---------------------------------------------------------------------------
+
+// p and ds of the 64 x 64 tile (rows r0.., keys k0..) into Ps and Ss [row][key].
+// Rows and keys outside the sequence, and masked pairs, give zeros.
+__device__ __forceinline__ void tile_grads(const LatentArgs &a, const float *Qs, const float *Ks, int ld, int D,
+                                           const float *Os, const float *Vs, int ldv, int Dv, const float *lse_s,
+                                           const float *delta_s, int r0, int k0, int lq, int lk, float *Ps, float *Ss) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float s[4][4] = {}, dp[4][4] = {};
+    dot44(s, Qs, ld, Ks, ld, D);
+    dot44(dp, Os, ldv, Vs, ldv, Dv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool on = seen(a, r0 + r, k0 + tx + 16 * j, lq, lk);
+            const float p = on ? expf(s[i][j] * a.scale - lse_s[r]) : 0.f;
+            if (Ps) Ps[r * kLdP + tx + 16 * j] = p;
+            Ss[r * kLdP + tx + 16 * j] = on ? p * (dp[i][j] - delta_s[r]) : 0.f;
+        }
+    }
+}
+
+__device__ __forceinline__ void load_stats(const LatentArgs &a, float *lse_s, float *delta_s, long row0, int rows, int h) {
+    if (threadIdx.x < kTile) {
+        const int r = threadIdx.x;
+        const size_t at = (size_t)(row0 + r) * a.H + h;
+        lse_s[r] = r < rows ? a.lse[at] : 0.f;
+        delta_s[r] = r < rows ? a.delta[at] : 0.f;
+    }
+}
+
+template <typename T, int ND, int NDV>
+__global__ void __launch_bounds__(kThreads) latent_dkv_f32_kernel(LatentArgs a) {
+    extern __shared__ __align__(16) float smem[];
+    constexpr int D = 64 * ND, ld = D + 4, Dv = 64 * NDV, ldv = Dv + 4;
+    float *Ks = smem, *Vs = Ks + kTile * ld, *Qs = Vs + kTile * ldv, *Os = Qs + kTile * ld, *Ps = Os + kTile * ldv,
+          *Ss = Ps + kTile * kLdP, *lse_s = Ss + kTile * kLdP, *delta_s = lse_s + kTile;
+    int t;
+    const int n = find_tile(a.cu_k, a.num_seqs, a.total_k, kTile, (int)blockIdx.x, &t);
+    const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
+    const int h = blockIdx.y, k0 = t * kTile;
+    const int keys = min(kTile, sk.len - k0);
+    if (keys <= 0) return;
+    load_rows<T>(Ks, ld, (const T *)a.k, a.Dk, (const T *)a.k_shared, a.Ds, 1, sk.start + k0, keys, a.H, h);
+    load_rows<T>(Vs, ldv, (const T *)a.v, Dv, (const T *)nullptr, 0, 1, sk.start + k0, keys, a.H, h);
+    float dk[4][ND][4] = {}, dv[4][NDV][4] = {};
+    // the first row that sees key k0
+    const int first = a.causal ? max(0, k0 - (sk.len - sq.len)) : 0;
+    for (int r0 = first / kTile * kTile; r0 < sq.len; r0 += kTile) {
+        const int rows = min(kTile, sq.len - r0);
+        __syncthreads();
+        load_rows<T>(Qs, ld, (const T *)a.q, a.Dk, (const T *)a.q_shared, a.Ds, a.H, sq.start + r0, rows, a.H, h);
+        load_rows<T>(Os, ldv, (const T *)a.d_out, Dv, (const T *)nullptr, 0, 1, sq.start + r0, rows, a.H, h);
+        load_stats(a, lse_s, delta_s, sq.start + r0, rows, h);
+        __syncthreads();
+        tile_grads(a, Qs, Ks, ld, D, Os, Vs, ldv, Dv, lse_s, delta_s, r0, k0, sq.len, sk.len, Ps, Ss);
+        __syncthreads();
+        cols_times<NDV>(dv, Ps, Os, ldv);
+        cols_times<ND>(dk, Ss, Qs, ld);
+    }
+    store_rows<T, T, NDV>(dv, 1.f, (T *)a.dv, Dv, (T *)nullptr, 0, sk.start + k0, keys, a.H, h);
+    store_rows<T, float, ND>(dk, a.scale, (T *)a.dk, a.Dk, a.dks_heads, a.Ds, sk.start + k0, keys, a.H, h);
+}
+
+template <typename T, int ND, int NDV>
+__global__ void __launch_bounds__(kThreads) latent_dq_f32_kernel(LatentArgs a) {
+    extern __shared__ __align__(16) float smem[];
+    constexpr int D = 64 * ND, ld = D + 4, Dv = 64 * NDV, ldv = Dv + 4;
+    float *Ks = smem, *Vs = Ks + kTile * ld, *Qs = Vs + kTile * ldv, *Os = Qs + kTile * ld, *Ss = Os + kTile * ldv,
+          *lse_s = Ss + kTile * kLdP, *delta_s = lse_s + kTile;
+    int t;
+    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, kTile, (int)(gridDim.x - 1 - blockIdx.x), &t);
+    const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
+    const int h = blockIdx.y, r0 = t * kTile;
+    const int rows = min(kTile, sq.len - r0);
+    if (rows <= 0) return;
+    load_rows<T>(Qs, ld, (const T *)a.q, a.Dk, (const T *)a.q_shared, a.Ds, a.H, sq.start + r0, rows, a.H, h);
+    load_rows<T>(Os, ldv, (const T *)a.d_out, Dv, (const T *)nullptr, 0, 1, sq.start + r0, rows, a.H, h);
+    load_stats(a, lse_s, delta_s, sq.start + r0, rows, h);
+    float dq[4][ND][4] = {};
+    const int kend = a.causal ? min(sk.len, r0 + rows + sk.len - sq.len) : sk.len;
+    for (int k0 = 0; k0 < kend; k0 += kTile) {
+        const int keys = min(kTile, sk.len - k0);
+        __syncthreads();
+        load_rows<T>(Ks, ld, (const T *)a.k, a.Dk, (const T *)a.k_shared, a.Ds, 1, sk.start + k0, keys, a.H, h);
+        load_rows<T>(Vs, ldv, (const T *)a.v, Dv, (const T *)nullptr, 0, 1, sk.start + k0, keys, a.H, h);
+        __syncthreads();
+        tile_grads(a, Qs, Ks, ld, D, Os, Vs, ldv, Dv, lse_s, delta_s, r0, k0, sq.len, sk.len, nullptr, Ss);
+        __syncthreads();
+        rows_times<ND>(dq, Ss, Ks, ld);
+    }
+    store_rows<T, T, ND>(dq, a.scale, (T *)a.dq, a.Dk, (T *)a.dq_shared, a.Ds, sq.start + r0, rows, a.H, h);
+}
+
+// delta_i = d_out_i . out_i: one warp per (row, head).
+template <typename T>
+__global__ void __launch_bounds__(256) latent_delta_kernel(const T *out, const T *d_out, float *delta, long rows, int Dv) {
+    const long r = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (r >= rows) return;
+    float x = 0.f;
+    for (int c = 4 * lane; c < Dv; c += 128) {
+        const float4 o = Io<T>::ld4(out + r * Dv + c), d = Io<T>::ld4(d_out + r * Dv + c);
+        x = fmaf(o.x, d.x, fmaf(o.y, d.y, fmaf(o.z, d.z, fmaf(o.w, d.w, x))));
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    if (lane == 0) delta[r] = x;
+}
+
+// dk_shared[row] = sum over heads of its per-head parts, heads in order.  Rows
+// that belong to no sequence are left as they were.
+template <typename T>
+__global__ void __launch_bounds__(256) latent_shared_sum_kernel(const float *parts, T *out, const int32_t *cu_k,
+                                                                int num_seqs, long rows, int H, int Ds) {
+    const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
+    const long row = e / Ds;
+    if (row >= rows || row >= cu_k[num_seqs]) return;
+    const int c = (int)(e % Ds);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int h = 0; h < H; ++h) {
+        const float4 y = *reinterpret_cast<const float4 *>(parts + ((size_t)row * H + h) * Ds + c);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    Io<T>::st4(out + row * Ds + c, x);
+}
+
+template <typename T, int NDV> cudaError_t forward_nv(const LatentArgs &a, cudaStream_t s) {
+    constexpr size_t most = sizeof(float) * kTile * (2 * (192 + 4) + (64 * NDV + 4) + kLdP);
+    const cudaError_t e = allow_smem<latent_forward_f32_kernel<T, NDV>>(most);
+    if (e != cudaSuccess) return e;
+    const size_t bytes = sizeof(float) * kTile * (2 * (a.Dk + a.Ds + 4) + (64 * NDV + 4) + kLdP);
+    const dim3 grid(tile_slots(a.total_q, a.num_seqs, kTile), a.H);
+    latent_forward_f32_kernel<T, NDV><<<grid, kThreads, bytes, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int ND, int NDV> cudaError_t backward_nd(const LatentArgs &a, cudaStream_t s) {
+    constexpr size_t tiles = 2 * (64 * ND + 4) + 2 * (64 * NDV + 4);
+    constexpr size_t bkv = sizeof(float) * kTile * (tiles + 2 * kLdP + 2), bq = sizeof(float) * kTile * (tiles + kLdP + 2);
+    cudaError_t e = allow_smem<latent_dkv_f32_kernel<T, ND, NDV>>(bkv);
+    if (e == cudaSuccess) e = allow_smem<latent_dq_f32_kernel<T, ND, NDV>>(bq);
+    if (e != cudaSuccess) return e;
+    if (a.total_k > 0) {
+        const dim3 grid(tile_slots(a.total_k, a.num_seqs, kTile), a.H);
+        latent_dkv_f32_kernel<T, ND, NDV><<<grid, kThreads, bkv, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (a.total_q > 0) {
+        const dim3 grid(tile_slots(a.total_q, a.num_seqs, kTile), a.H);
+        latent_dq_f32_kernel<T, ND, NDV><<<grid, kThreads, bq, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+template <typename T> cudaError_t backward_t(const LatentArgs &a, cudaStream_t s) {
+    const int nd = (a.Dk + a.Ds) / 64;
+    if (a.Dv == 64)
+        return nd == 1 ? backward_nd<T, 1, 1>(a, s) : nd == 2 ? backward_nd<T, 2, 1>(a, s) : backward_nd<T, 3, 1>(a, s);
+    return nd == 1 ? backward_nd<T, 1, 2>(a, s) : nd == 2 ? backward_nd<T, 2, 2>(a, s) : backward_nd<T, 3, 2>(a, s);
+}
+
+// ---------------------------------------------------------------------------
+// Absorbed form over pages.  One CTA per (split of a sequence, 16 query rows);
+// the splits' outputs and log-sum-exps are joined by a second kernel.
+// ---------------------------------------------------------------------------
+constexpr int kDecRows = 16, kDecTok = 32;
+
+template <typename T, int NL>      // Dl = 128 NL
+__global__ void __launch_bounds__(kThreads) latent_decode_f32_kernel(LatentDecodeArgs a, int splits) {
+    extern __shared__ __align__(16) float smem[];
+    constexpr int Dl = 128 * NL;
+    const int D = Dl + a.Ds, ld = D + 4;
+    float *Qs = smem, *Cs = Qs + kDecRows * ld, *Ps = Cs + kDecTok * ld, *stat = Ps + kDecRows * (kDecTok + 4);
+    // stat: rescaling factors of the tile [16]
+    const int b = blockIdx.x / splits, sp = blockIdx.x % splits, R = a.T * a.H, row0 = blockIdx.y * kDecRows;
+    const int rows = min(kDecRows, R - row0), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long most = (long)a.table_width * a.page_size;
+    const int given = a.lens[b];
+    const int len = (int)min((long)max(given, 0), most);
+    if ((given < 0 || given > most) && tid == 0) atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
+    const int tiles = (len + kDecTok - 1) / kDecTok;
+    const int t_lo = (int)((long)tiles * sp / splits), t_hi = (int)((long)tiles * (sp + 1) / splits);
+    for (int e = tid; e < kDecRows * D / 4; e += kThreads) {
+        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            const size_t row = (size_t)b * R + row0 + r;
+            x = c < Dl ? Io<T>::ld4((const T *)a.q + row * Dl + c) : Io<T>::ld4((const T *)a.q_shared + row * a.Ds + c - Dl);
+        }
+        *reinterpret_cast<float4 *>(Qs + r * ld + c) = x;
+    }
+    // scores: thread = 4 rows x 4 tokens over one of 8 slices of the columns
+    const int slice = lane & 7, blk = warp * 4 + (lane >> 3), br = (blk & 3) * 4, bt = (blk >> 2) * 4;
+    float m = -INFINITY, l = 0.f;                       // of row tid / 16 (16 threads each)
+    const int srow = tid >> 4, sc = tid & 15;
+    // outputs: thread = rows 8 (tid / 128) .. + 7, columns tid % 128 + 128 c
+    const int og = tid >> 7, oc = tid & 127;
+    float o[8][NL] = {};
+    for (int t = t_lo; t < t_hi; ++t) {
+        const int j0 = t * kDecTok;
+        __syncthreads();
+        for (int e = tid; e < kDecTok * D / 4; e += kThreads) {
+            const int r = e / (D / 4), c = (e % (D / 4)) * 4, j = j0 + r;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < len) {
+                const int page = a.table[(size_t)b * a.table_width + j / a.page_size];
+                if (page >= 0 && page < a.num_pages)
+                    x = Io<T>::ld4((const T *)a.pages + ((size_t)page * a.page_size + j % a.page_size) * D + c);
+                else if (c == 0)
+                    atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
+            }
+            *reinterpret_cast<float4 *>(Cs + r * ld + c) = x;
+        }
+        __syncthreads();
+        {
+            float s[4][4] = {};
+            for (int c = 4 * slice; c < D; c += 32) {
+                float4 x[4], y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = *reinterpret_cast<const float4 *>(Qs + (br + i) * ld + c);
+                    y[i] = *reinterpret_cast<const float4 *>(Cs + (bt + i) * ld + c);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, s[i][j]))));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                    for (int off = 4; off; off >>= 1) s[i][j] += __shfl_xor_sync(0xffffffffu, s[i][j], off);
+                    if (slice == 0) Ps[(br + i) * (kDecTok + 4) + bt + j] = s[i][j];
+                }
+        }
+        __syncthreads();
+        {
+            // row srow by 16 threads of two tokens each
+            const int last = len - a.T + (row0 + srow) / a.H;     // the last token this row sees
+            float x[2], top = m;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int j = j0 + sc + 16 * u;
+                bool on = j <= last && j < len && srow < rows;
+                if (on) {
+                    const int page = a.table[(size_t)b * a.table_width + j / a.page_size];
+                    on = page >= 0 && page < a.num_pages;
+                }
+                x[u] = on ? Ps[srow * (kDecTok + 4) + sc + 16 * u] * a.scale : -INFINITY;
+                top = fmaxf(top, x[u]);
+            }
+#pragma unroll
+            for (int off = 8; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float base = top == -INFINITY ? 0.f : top;
+            const float keep = expf(m - base);
+            m = top;
+            l *= keep;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float p = expf(x[u] - base);
+                l += p;
+                Ps[srow * (kDecTok + 4) + sc + 16 * u] = p;
+            }
+            if (sc == 0) stat[srow] = keep;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float keep = stat[8 * og + i];
+#pragma unroll
+            for (int c = 0; c < NL; ++c) o[i][c] *= keep;
+        }
+#pragma unroll 2
+        for (int j = 0; j < kDecTok; j += 4) {
+            float y[4][NL];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int c = 0; c < NL; ++c) y[u][c] = Cs[(j + u) * ld + oc + 128 * c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 p = *reinterpret_cast<const float4 *>(Ps + (8 * og + i) * (kDecTok + 4) + j);
+#pragma unroll
+                for (int c = 0; c < NL; ++c)
+                    o[i][c] = fmaf(p.x, y[0][c], fmaf(p.y, y[1][c], fmaf(p.z, y[2][c], fmaf(p.w, y[3][c], o[i][c]))));
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 8; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    __syncthreads();
+    if (sc == 0) {
+        stat[srow] = l > 0.f ? 1.f / l : 0.f;
+        const float lse = l > 0.f ? m + logf(l) : -INFINITY;
+        if (srow < rows) {
+            const size_t row = (size_t)b * R + row0 + srow;
+            if (splits > 1) a.part[row * splits + sp] = lse;
+            else if (a.lse) a.lse[row] = lse;
+        }
+    }
+    __syncthreads();
+    float *po = a.part + (((size_t)a.B * R * splits + 3) & ~(size_t)3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (8 * og + i >= rows) continue;
+        const size_t row = (size_t)b * R + row0 + 8 * og + i;
+        const float f = stat[8 * og + i];
+#pragma unroll
+        for (int c = 0; c < NL; ++c) {
+            if (splits > 1) po[(row * splits + sp) * Dl + oc + 128 * c] = o[i][c] * f;
+            else Io<T>::st((T *)a.out + row * Dl + oc + 128 * c, o[i][c] * f);
+        }
+    }
+}
+
+// out = sum_s e^{lse_s - lse} o_s, lse = log sum_s e^{lse_s}: one CTA per row.
+template <typename T>
+__global__ void __launch_bounds__(128) latent_join_kernel(LatentDecodeArgs a, int splits) {
+    const size_t row = blockIdx.x;
+    const float *ls = a.part + row * splits;
+    const float *po = a.part + (((size_t)a.B * a.T * a.H * splits + 3) & ~(size_t)3) + row * splits * a.Dl;
+    float top = -INFINITY, sum = 0.f;
+    for (int s = 0; s < splits; ++s) top = fmaxf(top, ls[s]);
+    const float base = top == -INFINITY ? 0.f : top;
+    for (int s = 0; s < splits; ++s) sum += expf(ls[s] - base);
+    const float f = sum > 0.f ? 1.f / sum : 0.f;
+    for (int c = threadIdx.x * 4; c < a.Dl; c += 512) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < splits; ++s) {
+            const float w = expf(ls[s] - base) * f;
+            const float4 y = *reinterpret_cast<const float4 *>(po + (size_t)s * a.Dl + c);
+            x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
+        }
+        Io<T>::st4((T *)a.out + row * a.Dl + c, x);
+    }
+    if (threadIdx.x == 0 && a.lse) a.lse[row] = sum > 0.f ? base + logf(sum) : -INFINITY;
+}
+
+// Enough splits that two CTAs per SM have work, at most 64.
+int decode_splits(int B, int rows) {
+    const long units = (long)B * ((rows + kDecRows - 1) / kDecRows);
+    const long want = (296 + units - 1) / units;
+    return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+}
+
+template <typename T, int NL> cudaError_t decode_nl(const LatentDecodeArgs &a, cudaStream_t s) {
+    constexpr size_t extra = kDecRows * (kDecTok + 4) + kDecRows;
+    constexpr size_t most = sizeof(float) * ((kDecRows + kDecTok) * (128 * NL + 64 + 4) + extra);
+    cudaError_t e = allow_smem<latent_decode_f32_kernel<T, NL>>(most);
+    if (e != cudaSuccess) return e;
+    const int R = a.T * a.H, splits = decode_splits(a.B, R);
+    const size_t bytes = sizeof(float) * ((kDecRows + kDecTok) * (128 * NL + a.Ds + 4) + extra);
+    latent_decode_f32_kernel<T, NL><<<dim3(splits * a.B, (R + kDecRows - 1) / kDecRows), kThreads, bytes, s>>>(a, splits);
+    if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
+    latent_join_kernel<T><<<a.B * R, 128, 0, s>>>(a, splits);
+    return cudaGetLastError();
+}
+template <typename T> cudaError_t decode_t(const LatentDecodeArgs &a, cudaStream_t s) {
+    switch (a.Dl / 128) {
+        case 1: return decode_nl<T, 1>(a, s);
+        case 2: return decode_nl<T, 2>(a, s);
+        case 3: return decode_nl<T, 3>(a, s);
+        default: return decode_nl<T, 4>(a, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_forward_f32(const LatentArgs &a, cudaStream_t s) {
+    if (a.dtype == RDA_F32) return a.Dv == 64 ? forward_nv<float, 1>(a, s) : forward_nv<float, 2>(a, s);
+    return a.Dv == 64 ? forward_nv<__nv_bfloat16, 1>(a, s) : forward_nv<__nv_bfloat16, 2>(a, s);
+}
+
+cudaError_t launch_latent_delta(const LatentArgs &a, cudaStream_t s) {
+    const long rows = (long)a.total_q * a.H;
+    const unsigned grid = (unsigned)((rows + 7) / 8);
+    if (!grid) return cudaSuccess;
+    if (a.dtype == RDA_F32)
+        latent_delta_kernel<float><<<grid, 256, 0, s>>>((const float *)a.out, (const float *)a.d_out, a.delta, rows, a.Dv);
+    else
+        latent_delta_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>((const __nv_bfloat16 *)a.out,
+                                                               (const __nv_bfloat16 *)a.d_out, a.delta, rows, a.Dv);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_latent_shared_sum(const LatentArgs &a, cudaStream_t s) {
+    const long n = (long)a.total_k * a.Ds / 4;
+    const unsigned grid = (unsigned)((n + 255) / 256);
+    if (!grid) return cudaSuccess;
+    if (a.dtype == RDA_F32)
+        latent_shared_sum_kernel<float><<<grid, 256, 0, s>>>(a.dks_heads, (float *)a.dk_shared, a.cu_k, a.num_seqs,
+                                                             a.total_k, a.H, a.Ds);
+    else
+        latent_shared_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a.dks_heads, (__nv_bfloat16 *)a.dk_shared, a.cu_k,
+                                                                    a.num_seqs, a.total_k, a.H, a.Ds);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_latent_backward_f32(const LatentArgs &a, cudaStream_t s) {
+    return a.dtype == RDA_F32 ? backward_t<float>(a, s) : backward_t<__nv_bfloat16>(a, s);
+}
+
+cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s) {
+    return a.dtype == RDA_F32 ? decode_t<float>(a, s) : decode_t<__nv_bfloat16>(a, s);
+}
+
+size_t latent_backward_scratch_bytes(int total_q, int total_k, int H, int Ds) {
+    const size_t d = ((size_t)total_q * H * sizeof(float) + 255) / 256 * 256;
+    return d + (size_t)total_k * H * Ds * sizeof(float);
+}
+
+size_t latent_decode_scratch_bytes(int B, int T, int H, int Dl) {
+    const int splits = decode_splits(B, T * H);
+    return splits == 1 ? 0 : ((size_t)B * T * H * splits * (Dl + 1) + 4) * sizeof(float);
+}
+
+}  // namespace rda

@@ -405,6 +405,123 @@ rda_status_t rda_prefill_chunked_noalloc(const void *q, const void *k, const voi
                                          void *stream);
 
 /*
+ * LATENT ATTENTION
+ *
+ * The hybrid's other layers (one in four, next to three RDA layers) are
+ * multi-head attention whose keys and values of all heads come from one latent
+ * vector a token, cached with a key part that the heads share: 576 values per
+ * token.  No positions enter (the article calls the layers NoPE).
+ *
+ * Expanded form, for prompts and training: per head, keys k and values v made
+ * from the latents by the caller, and the shared key part k~:
+ *     s_ij = scale (q_i . k_j + q~_i . k~_j)     over the keys j that query i sees
+ *     out_i = sum_j softmax_j(s_i)_j v_j,         lse_i = log sum_j e^{s_ij}
+ * Packed sequences as in rda_prefill_varlen; a sequence may have more keys than
+ * queries (a cached prefix) or fewer.  With `causal`, query i of lq sees the
+ * keys j <= i + lk - lq: the last query sees all.  A query that sees no key gives
+ * out = 0 and lse = -inf.
+ *
+ *   q [total_q,H,Dk], k [total_k,H,Dk], v [total_k,H,Dv], out [total_q,H,Dv]: device, dtype
+ *   q_shared [total_q,H,Ds], k_shared [total_k,Ds]: device, dtype; NULL exactly when Ds = 0
+ *   cu_seqlens_q, cu_seqlens_k  device int32 [num_seqs+1], non-decreasing from 0 to at most
+ *                  total_q, total_k (values are kept inside these bounds).  Rows
+ *                  behind the last sequence are neither read into a result nor written
+ *   lse            device fp32 [total_q,H] or NULL
+ *   Dk, Dv in {64, 128}, Ds in {0, 64}, H <= 1024; total * H * (Dk + Ds) < 2^31
+ * Preconditions, not checked: finite inputs within the sequences.  Sums, softmax
+ * statistics and (for fp32) products are fp32; bf16 inputs run on the tensor cores,
+ * with the probabilities rounded to bf16 for their product with v.
+ */
+size_t rda_latent_prefill_workspace_bytes(int total_q, int total_k, int H, int Dk, int Ds, int Dv, int num_seqs);
+
+rda_status_t rda_latent_prefill(const void *q, const void *q_shared, const void *k, const void *k_shared, const void *v,
+                                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                int num_seqs, int total_q, int total_k, void *out, float *lse,
+                                rda_dtype_t dtype, int H, int Dk, int Ds, int Dv, float scale, int causal,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of <d_out, out> of rda_latent_prefill, from its inputs and its results:
+ *     ds_ij = p_ij (d_out_i . v_j - d_out_i . out_i),  p_ij = e^{s_ij - lse_i}
+ *     dq = scale ds k,  dk = scale ds^T q,  dv = p^T d_out;  the same for the shared
+ *     parts, dk_shared summed over the heads
+ *   out, d_out  device, dtype, [total_q,H,Dv];  lse device fp32 [total_q,H]
+ *   dq, dq_shared, dk, dk_shared, dv  device, dtype, shaped like their inputs
+ *               (dq_shared, dk_shared NULL exactly when Ds = 0)
+ * Other arguments as above.  Every sum has a fixed order: results are reproducible
+ * bit for bit.  Queries and keys without a partner get zeros.
+ */
+size_t rda_latent_backward_workspace_bytes(int total_q, int total_k, int H, int Dk, int Ds, int Dv, int num_seqs);
+
+rda_status_t rda_latent_backward(const void *q, const void *q_shared, const void *k, const void *k_shared, const void *v,
+                                 const void *out, const float *lse, const void *d_out,
+                                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                 int num_seqs, int total_q, int total_k,
+                                 void *dq, void *dq_shared, void *dk, void *dk_shared, void *dv,
+                                 rda_dtype_t dtype, int H, int Dk, int Ds, int Dv, float scale, int causal,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Absorbed form, for decoding: the per-head maps to keys and values are taken
+ * into the queries and out of the results by the caller, so that all heads
+ * attend to the cached vectors c_j = [l_j, k~_j] themselves:
+ *     s_j = scale (q . l_j + q_shared . k~_j),  out = sum_j softmax(s)_j l_j
+ * for T new tokens per sequence (1 <= T <= 8, as rda_decode_tokens).  The new
+ * tokens' own vectors are already in the cache: query t sees the first
+ * seq_lens - T + t + 1 tokens (none: out = 0, lse = -inf).
+ *
+ *   q [B,T,H,Dl], q_shared [B,T,H,Ds] (NULL exactly when Ds = 0), out [B,T,H,Dl]: device, dtype
+ *   pages        device, dtype, [num_pages,page_size,Dl+Ds]; may hold anything, NaN
+ *                among it, in rows that belong to no cached token
+ *   block_table  device int32 [B,table_width]: page numbers of each sequence in order;
+ *                entries past a sequence's last page are not read
+ *   seq_lens     device int32 [B]
+ *   lse          device fp32 [B,T,H] or NULL
+ *   Dl in {128, 256, 384, 512}, Ds in {0, 64}, page_size a multiple of 16, H <= 1024, B <= 65535;
+ *   num_pages * page_size and table_width * page_size below 2^31 (the cache may have more
+ *   than 2^31 elements)
+ * A page number outside [0, num_pages) takes its tokens out of the sequence, and a
+ * length outside [0, table_width * page_size] is cut to it; either records
+ * RDA_ERR_INVALID_ARG in the workspace error word.
+ */
+size_t rda_latent_decode_workspace_bytes(int B, int T, int H, int Dl, int Ds);
+
+rda_status_t rda_latent_decode(const void *q, const void *q_shared, const void *pages, const int32_t *block_table,
+                               const int32_t *seq_lens, void *out, float *lse, rda_dtype_t dtype,
+                               int B, int T, int H, int Dl, int Ds, int num_pages, int page_size, int table_width,
+                               float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Verification of drafted tokens, after the target model has read them all in
+ * one pass (rda_decode_tokens, rda_latent_decode): speculative sampling from
+ * given random numbers.  Draft t of a sequence is kept iff all before it were and
+ *     u_t q_t(x_t) < p_t(x_t).
+ * After k kept drafts the next token is drawn with the last uniform u: the first i with
+ *     w_0 + .. + w_i > u (w_0 + .. + w_{V-1}),
+ * w = max(p_k - q_k, 0) at the first refusal (w = p_k where that is zero everywhere),
+ * w = p_k when every draft was kept.  The kept tokens then follow the target's
+ * distribution exactly.
+ *
+ *   draft_tokens  device int32 [B,T] (a token outside [0, V) is refused); NULL allowed when T = 0
+ *   draft_probs   device fp32 [B,T,V], or NULL: each draft was chosen outright (q = 1 at it)
+ *   target_probs  device fp32 [B,T+1,V], finite, not negative; need not be normalised
+ *   uniforms      device fp32 [B,T+1], each in [0, 1): one per draft, the last for the draw
+ *   num_drafts    device int32 [B] in [0, T] (kept inside it), or NULL: T drafts each
+ *   tokens        device int32 [B,T+1]: the kept drafts, the drawn token (-1 if no token
+ *                 weighs anything), then -1
+ *   num_accepted  device int32 [B]: k
+ *   0 <= T <= 32, B <= 65535
+ * A recurrent state that has read all T drafts is taken back to the kept ones by
+ * replaying rda_decode_tokens on the state from before with beta = 0 and
+ * log_alpha = 0 for the tokens that were not kept: they leave it unchanged.
+ */
+size_t rda_verify_drafts_workspace_bytes(int B, int T, int V);
+
+rda_status_t rda_verify_drafts(const int32_t *draft_tokens, const float *draft_probs, const float *target_probs,
+                               const float *uniforms, const int32_t *num_drafts, int32_t *tokens, int32_t *num_accepted,
+                               int B, int T, int V, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * TESTING ONLY: fault injection for the device-side timeout path.
  *
  * Process-wide; affects the prefill calls made after it returns.  The bound of
