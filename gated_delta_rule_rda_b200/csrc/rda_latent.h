@@ -103,10 +103,13 @@ cudaError_t launch_latent_backward_f32(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_latent_delta(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_latent_shared_sum(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s);
+// bf16: tensor cores
+cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s);
 
 size_t latent_backward_scratch_bytes(int total_q, int total_k, int H, int Ds);
 size_t latent_decode_scratch_bytes(int B, int T, int H, int Dl);
+size_t latent_decode_tc_scratch_bytes(int T, int H, int Dl, int Ds);
 size_t verify_scratch_bytes(int B, int V);
 
 }  // namespace rda

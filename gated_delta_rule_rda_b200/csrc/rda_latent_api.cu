@@ -125,7 +125,8 @@ size_t rda_latent_decode_workspace_bytes(int B, int T, int H, int Dl, int Ds) {
     if (B < 0 || T < 0 || T > kMaxDecodeTokens || H <= 0 || H > kMaxHeads || Dl <= 0 || Dl > 512 || Dl % 128 ||
         (Ds != 0 && Ds != 64))
         return 0;
-    return kErrorWordBytes + (B && T ? latent_decode_scratch_bytes(B, T, H, Dl) : 0);
+    if (!B || !T) return kErrorWordBytes;
+    return kErrorWordBytes + std::max(latent_decode_scratch_bytes(B, T, H, Dl), latent_decode_tc_scratch_bytes(T, H, Dl, Ds));
 }
 
 rda_status_t rda_latent_decode(const void *q, const void *q_shared, const void *pages, const int32_t *block_table,
@@ -158,7 +159,8 @@ rda_status_t rda_latent_decode(const void *q, const void *q_shared, const void *
     a.err = static_cast<int32_t *>(workspace);
     a.wait_ns = wait_settings().wait_ns;
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kErrorWordBytes);
-    return done(launch_latent_decode_f32(a, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return done(dtype == RDA_BF16 ? launch_latent_decode_tc(a, s) : launch_latent_decode_f32(a, s));
 }
 
 size_t rda_verify_drafts_workspace_bytes(int B, int T, int V) {

@@ -620,7 +620,7 @@ cudaError_t launch_latent_backward_f32(const LatentArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s) {
-    return a.dtype == RDA_F32 ? decode_t<float>(a, s) : decode_t<__nv_bfloat16>(a, s);
+    return decode_t<float>(a, s);
 }
 
 size_t latent_backward_scratch_bytes(int total_q, int total_k, int H, int Ds) {

@@ -1,0 +1,149 @@
+// What the latent-attention kernels share besides sm100_ptx.cuh: bounded waits,
+// the remaining tcgen05 forms, swizzled addressing and small conversions.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "rda.h"
+#include "sm100_ptx.cuh"
+
+namespace rda {
+namespace ptx {
+
+// Bounded mbarrier waits of one CTA.  `abort` is a word of shared memory: a
+// wait that runs out records RDA_ERR_TIMEOUT in *err and sets it; from then on
+// every wait of the CTA returns at once.  All threads run their loops to the
+// end either way (no thread leaves a named barrier short); MMAs and copies are
+// issued only while `ok` holds.
+struct Waiter {
+    volatile int *abort;
+    int32_t *err;
+    uint64_t limit_ns;
+
+    static __device__ __forceinline__ uint64_t now() {
+        uint64_t t;
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+        return t;
+    }
+    __device__ __noinline__ bool slow(uint64_t *bar, uint32_t parity) const {
+        const uint64_t t0 = now();
+        for (;;) {
+            if (*abort) return false;
+            for (int i = 0; i < 8; ++i)
+                if (mbar_try_wait(bar, parity)) return true;
+            if (now() - t0 > limit_ns) {
+                *abort = 1;
+                atomicCAS(err, 0, (int32_t)RDA_ERR_TIMEOUT);
+                return false;
+            }
+        }
+    }
+    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) const {
+        return mbar_try_wait(bar, parity) || slow(bar, parity);
+    }
+    // ignores the abort word: lets what is in flight land before the CTA leaves (bounded from t0 on)
+    __device__ __noinline__ void drain(uint64_t *bar, uint32_t parity, uint64_t t0) const {
+        while (!mbar_try_wait(bar, parity))
+            if (now() - t0 > limit_ns) return;
+    }
+};
+
+// A slot of a ring and the parity of its next phase.
+struct RingPos {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++slot == n) slot = 0, phase ^= 1;
+    }
+};
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate (A: one row per lane, two values a column).
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 16 lanes x 16 columns: thread l gets lanes l/4 and l/4 + 8 at columns 2(l%4), + 1 of both 8-column blocks.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, float *v) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 32 lanes x 32 bits, 32 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float *v) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+    tmem_st16(taddr, r);
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Four 8x8 matrices of 16-bit values, each stored transposed: row r of matrix m at the address that lane
+// 8 m + r gives; register m holds (row l/4, columns 2(l%4), + 1) of the untransposed matrix.
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r0), "r"(r1),
+                 "r"(r2), "r"(r3)
+                 : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// Byte offset of 16-byte chunk `c` (0..7) of row `row` in a tile of 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t c) { return row * 128 + ((c ^ (row & 7)) << 4); }
+
+// The dynamic shared memory rounded up to 1024 bytes, as shared memory.
+__device__ __forceinline__ uint8_t *align_1024(uint8_t *raw) { return raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u); }
+
+}  // namespace ptx
+
+// A bf16 tensor [d2][d1][d0] (contiguous rows of d0, strides in elements) as a
+// TMA map with boxes of 64 x box1 x box2, 128-byte swizzle, zeros outside.
+bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
+                 uint64_t stride2, uint32_t box1, uint32_t box2);
+
+}  // namespace rda
