@@ -24,7 +24,7 @@
 //   warp 0      producer: pages by TMA (one box per 16..64 rows of a page), Q
 //   warp 1      one thread issues the MMAs: the next tile's scores before this
 //               tile's values, so that the tensor pipe works while softmax runs
-//   warps 2..5  softmax: running maximum and sum per row (a column of S^T: over
+//   warps 2..   softmax, four warps (16 rows) or eight (each four take half of the rows): running maximum and sum per row (a column of S^T: over
 //               lanes by shuffles, over warps through shared memory); P^T goes to
 //               shared memory; O^T stays in TMEM and is rescaled only when a
 //               maximum has grown by more than 2^8
@@ -45,25 +45,27 @@ using namespace ptx;
 
 constexpr int kTok = 64;                 // tokens per tile
 constexpr int kCtas = 148;               // one CTA per SM
-constexpr int kThreads = 192;
-constexpr uint32_t kPair = 16384;        // slot: 64 tokens x 128 latent columns
+constexpr int kScan = 192;               // threads that sum up the lengths
+constexpr uint32_t kPair = 16384;        // 64 tokens x 128 latent columns; a slot is one or two of them
 constexpr uint32_t kBox = 8192;          // 64 tokens x 64 columns
-constexpr int kMaxPairs = 12, kMaxShared = 2;
-constexpr int kInfo = 16;                // tiles whose masks are kept (the ring holds at most kMaxPairs)
+constexpr int kMaxSlots = 12, kMaxShared = 2;
+constexpr int kLens = 256;               // batches up to this keep their lengths in shared memory
+constexpr int kInfo = 16;                // tiles whose masks are kept (the ring holds at most kMaxSlots)
 constexpr float kGrow = 8.f;             // rescale O when a maximum has grown by more (log2)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Shared memory behind the operand areas.
 template <int NT> struct Small {
-    uint64_t full[kMaxPairs], empty[kMaxPairs], sfull[kMaxShared], sempty[kMaxShared];
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t q_full, q_empty, s_full[2], p_ready, pv_done, o_empty;
     uint64_t info[kInfo];
     float wmax[2][4][NT];
     float lsum[4][NT];
     float factor[NT];
-    long long sums[kThreads];
+    long long sums[kScan];
     long long total, lo, hi;
     int first_b, first_off;
+    int lens[kLens];
     uint32_t tmem;
     volatile int abort;
 };
@@ -71,12 +73,12 @@ template <int NT> struct Small {
 struct Geometry {
     int rt, rows, nt;                    // row tiles, rows of a tile, columns of its MMAs
     int groups;                          // CTAs along the tiles
-    int pairs, shared;                   // ring slots
+    int slots, sp, shared;               // ring slots, pairs of a slot, slots of shared columns
     uint32_t smem;
 };
 
 struct Maps {
-    CUtensorMap pages, q, q_shared;
+    CUtensorMap pages, pages_shared, q, q_shared;
 };
 
 __host__ __device__ inline uint32_t operand_bytes(int nt, int D, int pairs, int shared) {
@@ -101,7 +103,7 @@ __host__ __device__ inline Parts parts_of(float *base, const Geometry &g, int Dl
 struct Args {
     LatentDecodeArgs a;
     Geometry g;
-    int box_rows;
+    int box_rows, chunks;                // rows and 64-column chunks of one copy
     int pages_bound;                     // first page coordinate outside the map
 };
 
@@ -118,10 +120,11 @@ struct Walk {
     int b, off;                          // next sequence, tiles of it already behind
     int len, tiles, t0, t1;              // the current segment: tiles [t0, t1) of sequence `seq`
     int seq;
+    const int *lens;                     // all of them in shared memory, or null
     __device__ __forceinline__ bool next(const LatentDecodeArgs &a) {
         if (pos >= hi) return false;
         seq = b;
-        len = seq_len(a, b);
+        len = lens ? lens[b] : seq_len(a, b);
         tiles = seq_tiles(len);
         t0 = off;
         t1 = (int)min((long long)tiles, off + (hi - pos));
@@ -132,15 +135,270 @@ struct Walk {
     }
 };
 
+// Rows 0 .. rows - 1 of O (columns of O^T in TMEM), times their factors: out[r][128 p + lane ..].
+template <int NT, int NC, typename T, typename F>
+__device__ __forceinline__ void store_result(uint32_t t_o, int NP, int rows, const float *factor, T *out, int stride, F conv) {
+#pragma unroll 1
+    for (int c = 0; c < NC; c += 16) {
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = factor[c + i];
+#pragma unroll 1
+        for (int p = 0; p < NP; ++p) {
+            float x[16];
+            tmem_ld16(t_o + p * NT + c, x);
+            tmem_wait_ld();
+            T *o = out + c * stride + 128 * p;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, o += stride)
+                if (c + i < rows) *o = conv(x[i] * f[i]);
+        }
+    }
+}
+
+// Columns of S^T (rows of the result) that the first four softmax warps take; four more take the rest.
+__host__ __device__ constexpr int split_cols(int nt) { return nt == 16 ? 16 : nt == 48 ? 32 : nt / 2; }
+__host__ __device__ constexpr int softmax_warps(int nt) { return nt == 16 ? 4 : 8; }
+
+template <int NT> struct SoftmaxCtx {
+    Small<NT> &S;
+    const Args &args;
+    Walk walk;
+    Waiter w;
+    uint8_t *pair_s, *p_s;
+    uint32_t tmem;
+    int rt, grp, rows, row0;
+    long long hi, total;
+};
+
+// Four warps on the columns [c0, c0 + NC) of S^T and O^T, c0 = 0 or split_cols(NT) (half 0 or 1).
+template <int NT, int NC>
+__device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
+    Small<NT> &S = x_.S;
+    const Args &args = x_.args;
+    const LatentDecodeArgs &a = args.a;
+    const Geometry &g = args.g;
+    const Waiter w = x_.w;
+    Walk walk = x_.walk;
+    uint8_t *pair_s = x_.pair_s, *p_s = x_.p_s;
+    const int NP = a.Dl / 128, NS = NP / g.sp, R = a.T * a.H;
+    const int rt = x_.rt, grp = x_.grp, row0 = x_.row0, rows = x_.rows;
+    const long long hi = x_.hi, total = x_.total;
+    const int c0 = half ? split_cols(NT) : 0, bar = 1 + half;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kSoft = 32 * softmax_warps(NT);
+    const uint32_t t_o = x_.tmem + c0, t_s = x_.tmem + 4 * NT + c0;
+    const int quad = warp & 3;                       // tokens 16 quad .. + 15 of a tile
+    const int tok = lane >> 2, col = 2 * (lane & 3); // my tokens: tok, tok + 8; my columns: 8 c + col, + 1
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const float sc = a.scale * kLog2e;
+    constexpr int C = NC / 8;
+    uint32_t it = 0;
+    const Parts parts = parts_of(a.part, g, a.Dl);
+    bool first_segment = true;
+    while (walk.next(a)) {
+        float m[C][2], l[C][2];
+        int last[C][2];                              // last token that my columns see
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                m[c][u] = -INFINITY;
+                l[c][u] = 0.f;
+                const int r = c0 + 8 * c + col + u;
+                last[c][u] = r < rows ? walk.len - a.T + (row0 + r) / a.H : -1;
+            }
+        const int all_see = rows > 0 ? walk.len - a.T + row0 / a.H : -1;     // what every row sees
+        for (int t = walk.t0; t < walk.t1; ++t, ++it) {
+            w.wait(&S.s_full[it & 1], (it >> 1) & 1);
+            tc_fence_after();
+            float v[C][4];
+#pragma unroll
+            for (int c = 0; c < C; c += 2) tmem_ld_16x256b_x2(t_s + (it & 1) * NT + 8 * c + lanes, &v[c][0]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[c][u] *= sc;       // log2 units; sc may be negative
+            const uint64_t valid = S.info[it % kInfo];
+            const int j0 = t * kTok + 16 * quad + tok;
+            const bool whole = valid == ~0ull && t * kTok + kTok - 1 <= all_see;
+            if (!whole) {
+                const bool v0 = valid >> (16 * quad + tok) & 1, v1 = valid >> (16 * quad + tok + 8) & 1;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (!v0 || j0 > last[c][u]) v[c][u] = -INFINITY;
+                        if (!v1 || j0 + 8 > last[c][u]) v[c][2 + u] = -INFINITY;
+                    }
+                // rows behind the sequence's end in a page may hold anything: 0 x NaN must not reach O
+                const int left = walk.len - t * kTok;
+                if (left < kTok) {
+                    const int from = max(left, 0);
+                    const int n = (min(kTok, (from + args.box_rows - 1) / args.box_rows * args.box_rows) - from) * 16;
+                    // the ring's slots are consecutive pairs of columns
+                    int pair = (int)((unsigned long long)it * NS % g.slots) * g.sp;
+                    for (int p = 0; p < NP; ++p) {
+                        uint8_t *base = pair_s + pair * kPair;
+                        for (int e = threadIdx.x - 64; e < n; e += kSoft)
+                            *reinterpret_cast<uint4 *>(base + ((e >> 3) & 1) * kBox + sw128(from + (e >> 4), e & 7)) =
+                                make_uint4(0, 0, 0, 0);
+                        if (++pair == g.slots * g.sp) pair = 0;
+                    }
+                }
+            }
+            // the tile's maximum of each of my columns
+            float top[C][2];
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float x = fmaxf(v[c][u], v[c][2 + u]);
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    top[c][u] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                }
+            if (lane < 4)
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    *reinterpret_cast<float2 *>(&S.wmax[it & 1][quad][c0 + 8 * c + col]) = make_float2(top[c][0], top[c][1]);
+            named_bar_sync(bar, 128);
+            bool grown = false;
+            float f[C][2];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float2 x[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<float2 *>(&S.wmax[it & 1][q][c0 + 8 * c + col]);
+                top[c][0] = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
+                top[c][1] = fmaxf(fmaxf(x[0].y, x[1].y), fmaxf(x[2].y, x[3].y));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float now = top[c][u];
+                    f[c][u] = 1.f;
+                    if (now > m[c][u] + kGrow || (m[c][u] == -INFINITY && now > -INFINITY)) {
+                        f[c][u] = ex2(m[c][u] - now);
+                        m[c][u] = now;
+                        grown = true;
+                    }
+                }
+            }
+            const bool rescale = __any_sync(0xffffffffu, grown) && t != walk.t0;
+            // P^T, and my part of the sums
+            uint32_t pk[C][2];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                float p[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) p[u] = m[c][u & 1] == -INFINITY ? 0.f : ex2(v[c][u] - m[c][u & 1]);
+                l[c][0] = fmaf(l[c][0], f[c][0], p[0] + p[2]);
+                l[c][1] = fmaf(l[c][1], f[c][1], p[1] + p[3]);
+                pk[c][0] = pack2(p[0], p[1]);
+                pk[c][1] = pack2(p[2], p[3]);
+            }
+            if (it > 0) w.wait(&S.pv_done, (it - 1) & 1);       // P and O^T are free
+            tc_fence_after();
+            if (rescale) {
+                if (quad == 0 && lane < 4)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        S.factor[c0 + 8 * c + col] = f[c][0];
+                        S.factor[c0 + 8 * c + col + 1] = f[c][1];
+                    }
+                named_bar_sync(bar, 128);
+                for (int p = 0; p < NP; ++p)
+#pragma unroll
+                    for (int c = 0; c < NC; c += 16) {
+                        float x[16];
+                        tmem_ld16(t_o + p * NT + c + lanes, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] *= S.factor[c0 + c + i];
+                        tmem_st16f(t_o + p * NT + c + lanes, x);
+                    }
+                tmem_wait_st();
+                named_bar_sync(bar, 128);                          // factors read by all
+            }
+#pragma unroll
+            for (int c = 0; c < C; c += 2) {
+                // matrices: (block c, tokens 0-7), (c, 8-15), (c + 1, 0-7), (c + 1, 8-15) of my warp's 16
+                const int r = c0 + 8 * (c + (lane >> 4)) + (lane & 7), ch = 2 * quad + ((lane >> 3) & 1);
+                stsm_x4_t(smem_u32(p_s) + sw128(r, ch), pk[c][0], pk[c][1], pk[c + 1][0], pk[c + 1][1]);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            mbar_arrive(&S.p_ready);
+        }
+        // the segment's result: whole, or one part of a sequence
+        const bool done = walk.t0 == 0 && walk.t1 == walk.tiles;
+        const size_t slot = ((size_t)grp * g.rt + rt) * 2 + (first_segment ? 0 : 1);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float x = l[c][u];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                if (lane < 4) S.lsum[quad][c0 + 8 * c + col + u] = x;
+            }
+        named_bar_sync(bar, 128);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int r = c0 + 8 * c + col + u;
+                const float x = (S.lsum[0][r] + S.lsum[1][r]) + (S.lsum[2][r] + S.lsum[3][r]);
+                if (quad == 0 && lane < 4) {
+                    S.factor[r] = x > 0.f ? 1.f / x : 0.f;
+                    const float lse = x > 0.f ? (m[c][u] + lg2(x)) * kLn2 : -INFINITY;
+                    if (r < rows) {
+                        if (!done) parts.lse[slot * NT + r] = lse;
+                        else if (a.lse) a.lse[(size_t)walk.seq * R + row0 + r] = lse;
+                    }
+                }
+            }
+        w.wait(&S.pv_done, (it - 1) & 1);
+        tc_fence_after();
+        named_bar_sync(bar, 128);
+        if (done) {
+            auto *o = static_cast<__nv_bfloat16 *>(a.out) + ((size_t)walk.seq * R + row0 + c0) * a.Dl + 32 * quad + lane;
+            store_result<NT, NC>(t_o + lanes, NP, rows - c0, S.factor + c0, o, a.Dl,
+                             [](float x) { return __float2bfloat16_rn(x); });
+        } else {
+            store_result<NT, NC>(t_o + lanes, NP, rows - c0, S.factor + c0, parts.o + (slot * NT + c0) * a.Dl + 32 * quad + lane, a.Dl,
+                             [](float x) { return x; });
+        }
+        tc_fence_before();
+        mbar_arrive(&S.o_empty);
+        named_bar_sync(bar, 128);                                  // factors are free again
+        if (rt == 0 && threadIdx.x == 64 && walk.pos >= hi) {
+            // this group's last segment: does its sequence begin here and go on in others?
+            int4 rec = make_int4(-1, 0, 0, 0);
+            if (!done && walk.t0 == 0) {
+                const long long groups = min((long long)g.groups, total);
+                const long long end = hi - walk.t1 + walk.tiles - 1;      // the sequence's last tile
+                long long gl = min(groups - 1, end * groups / total);     // the group that holds it
+                while (gl + 1 < groups && total * (gl + 1) / groups <= end) ++gl;
+                while (total * gl / groups > end) --gl;
+                rec = make_int4(walk.seq, (int)gl, first_segment ? 0 : 1, 0);
+            }
+            parts.rec[grp] = rec;
+        }
+        first_segment = false;
+    }
+}
+
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid_constant__ Maps maps, const Args args) {
+__global__ void __launch_bounds__(64 + 32 * softmax_warps(NT), 1) latent_decode_kernel(const __grid_constant__ Maps maps, const Args args) {
     extern __shared__ uint8_t smem_raw[];
     const LatentDecodeArgs &a = args.a;
     const Geometry &g = args.g;
     uint8_t *sm = align_1024(smem_raw);
-    const int NP = a.Dl / 128, NB = (a.Dl + a.Ds) / 64;
-    uint8_t *q_s = sm, *p_s = q_s + NB * NT * 128, *pair_s = p_s + NT * 128, *shared_s = pair_s + g.pairs * kPair;
-    Small<NT> &S = *reinterpret_cast<Small<NT> *>(shared_s + g.shared * kBox);
+    const int NP = a.Dl / 128, NB = (a.Dl + a.Ds) / 64, NS = NP / g.sp;    // pairs, boxes, slots of a tile
+    uint8_t *q_s = sm, *p_s = q_s + NB * NT * 128, *pair_s = p_s + NT * 128, *shared_s = pair_s + g.slots * g.sp * kPair;
+    Small<NT> &S = *reinterpret_cast<Small<NT> *>(shared_s + (a.Ds ? g.shared * kBox : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % g.rt, grp = blockIdx.x / g.rt;
     const int R = a.T * a.H, row0 = rt * g.rows, rows = min(g.rows, R - row0);
@@ -153,32 +411,36 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         tmem_relinquish();
     }
     if (tid == 32) {
-        for (int i = 0; i < g.pairs; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], 1);
-        for (int i = 0; i < g.shared; ++i) mbar_init(&S.sfull[i], 1), mbar_init(&S.sempty[i], 1);
+        for (int i = 0; i < g.slots; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], 1);
         mbar_init(&S.q_full, 1);
         mbar_init(&S.q_empty, 1);
         mbar_init(&S.s_full[0], 1);
         mbar_init(&S.s_full[1], 1);
-        mbar_init(&S.p_ready, 128);
+        mbar_init(&S.p_ready, 32 * softmax_warps(NT));
         mbar_init(&S.pv_done, 1);
-        mbar_init(&S.o_empty, 128);
+        mbar_init(&S.o_empty, 32 * softmax_warps(NT));
         S.abort = 0;
         fence_mbar_init();
         prefetch_tensormap(&maps.pages);
         prefetch_tensormap(&maps.q);
     }
     // this group's range of the tiles of all sequences
-    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    const int per = (a.B + kScan - 1) / kScan, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     {
         long long x = 0;
-        for (int b = b0; b < b1; ++b) x += seq_tiles(seq_len(a, b));
-        S.sums[tid] = x;
+        for (int b = b0; b < b1; ++b) {
+            const int given = a.lens[b], len = max(0, min(given, a.table_width * a.page_size));
+            if (given != len && blockIdx.x == 0) atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
+            if (a.B <= kLens) S.lens[b] = len;
+            x += seq_tiles(len);
+        }
+        if (tid < kScan) S.sums[tid] = x;
     }
     __syncthreads();
     if (warp == 0) {
-        long long part[kThreads / 32], x = 0;
+        long long part[kScan / 32], x = 0;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) part[i] = S.sums[lane * (kThreads / 32) + i], x += part[i];
+        for (int i = 0; i < kScan / 32; ++i) part[i] = S.sums[lane * (kScan / 32) + i], x += part[i];
         long long incl = x;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -187,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         }
         long long before = incl - x;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) {
-            S.sums[lane * (kThreads / 32) + i] = before;
+        for (int i = 0; i < kScan / 32; ++i) {
+            S.sums[lane * (kScan / 32) + i] = before;
             before += part[i];
         }
         if (lane == 31) {
@@ -200,11 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     }
     __syncthreads();
     const long long lo = S.lo, hi = S.hi, total = S.total;
-    if (lo < hi && lo >= S.sums[tid]) {
+    if (lo < hi && tid < kScan && lo >= S.sums[tid]) {
         // the thread whose sequences hold tile lo looks for it
         long long at = S.sums[tid];
         for (int b = b0; b < b1; ++b) {
-            const int n = seq_tiles(seq_len(a, b));
+            const int n = seq_tiles(a.B <= kLens ? S.lens[b] : seq_len(a, b));
             if (lo < at + n) {
                 S.first_b = b;
                 S.first_off = (int)(lo - at);
@@ -218,123 +480,170 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     tc_fence_after();
     const uint32_t tmem = S.tmem;
     const uint32_t t_o = tmem, t_s = tmem + 4 * NT;
-    Walk walk{lo, hi, lo < hi ? S.first_b : 0, lo < hi ? S.first_off : 0, 0, 0, 0, 0, 0};
+    Walk walk{lo, hi, lo < hi ? S.first_b : 0, lo < hi ? S.first_off : 0, 0, 0, 0, 0, 0,
+              a.B <= kLens ? S.lens : nullptr};
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        RingPos pr, sr;
-        uint32_t seg = 0, it = 0;
-        const int ng = kTok / args.box_rows;           // row boxes of a tile
-        const int mine = lane % ng;
-        const long long most = (long long)a.table_width * a.page_size;
-        while (walk.next(a)) {
-            if (rt == 0 && walk.t0 == 0 && lane == 0) {
-                const int given = a.lens[walk.seq];
-                if (given < 0 || given > most) atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
-            }
-            const int32_t *table = a.table + (size_t)walk.seq * a.table_width;
-            // my row box of tile t: its page, or one outside the map (zeros)
-            auto page_of = [&](int t) {
-                const int j = t * kTok + mine * args.box_rows;
-                return t < walk.t1 && j < walk.len ? table[j / a.page_size] : -1;
-            };
-            int page = page_of(walk.t0);
-            // lane 0 waits for room and announces the bytes; false once the CTA has given up
-            auto room = [&](uint64_t *empty, uint32_t parity, bool used, uint64_t *full, uint32_t bytes) {
-                bool go = true;
-                if (lane == 0) {
-                    go = (!used || w.wait(empty, parity)) && !S.abort;
-                    if (go) mbar_arrive_expect_tx(full, bytes);
+        if (elect_one()) {
+            RingPos pr;
+            int sr = 0;
+            uint32_t seg = 0, it = 0;
+            const int ng = kTok / args.box_rows;           // row boxes of a tile: 1, 2 or 4
+            bool go = true;
+            int page_next[4];                              // of the tile that comes next, of this sequence or the next one
+            auto look_up = [&](const Walk &x, int t) {
+                const int32_t *table = a.table + (size_t)x.seq * a.table_width;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = t * kTok + i * args.box_rows;
+                    page_next[i] = i < ng && j < x.len ? table[j / a.page_size] : -1;
                 }
-                return __shfl_sync(0xffffffffu, go, 0) != 0;
             };
-            if (room(&S.q_empty, (seg - 1) & 1, seg > 0, &S.q_full, NB * NT * 128)) {
-                if (lane < NB) {
-                    const int c = lane * 64, r = walk.seq * R + row0;
-                    if (c < a.Dl) tma_load_3d(q_s + lane * NT * 128, &maps.q, &S.q_full, c, r, 0);
-                    else tma_load_3d(q_s + lane * NT * 128, &maps.q_shared, &S.q_full, c - a.Dl, r, 0);
-                }
-                ++seg;
-            }
-            for (int t = walk.t0; t < walk.t1; ++t, ++it) {
-                const int j = t * kTok + mine * args.box_rows;
-                const bool ok = page >= 0 && page < a.num_pages;
-                if (!ok && j < walk.len && lane < ng) atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
-                const unsigned good = __ballot_sync(0xffffffffu, ok && lane < ng);
-                const int px = ok ? page : args.pages_bound, row = j % a.page_size;
-                page = page_of(t + 1);
-                if (lane == 0) {
+            bool more = walk.next(a);
+            if (more) look_up(walk, walk.t0);
+            while (more) {
+                Walk after = walk;
+                const bool another = after.next(a);
+                for (int t = walk.t0; t < walk.t1; ++t, ++it) {
+                    // a page outside the cache, or behind the end: a coordinate outside the map (zeros)
+                    int row[4], page[4];
                     uint64_t m = 0;
-                    for (int i = 0; i < ng; ++i)
-                        if (good >> i & 1)
-                            m |= (args.box_rows == 64 ? ~0ull : (1ull << args.box_rows) - 1) << (i * args.box_rows);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = t * kTok + i * args.box_rows;
+                        row[i] = j % a.page_size;
+                        page[i] = page_next[i];
+                        if (page[i] >= 0 && page[i] < a.num_pages) {
+                            if (i < ng) m |= (args.box_rows == 64 ? ~0ull : (1ull << args.box_rows) - 1) << (i * args.box_rows);
+                        } else {
+                            if (i < ng && j < walk.len) atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
+                            page[i] = args.pages_bound;
+                        }
+                    }
+                    if (t + 1 < walk.t1) look_up(walk, t + 1);
+                    else if (another) look_up(after, after.t0);
                     const int left = walk.len - t * kTok;
                     if (left < kTok) m &= left <= 0 ? 0ull : (1ull << left) - 1;
                     S.info[it % kInfo] = m;
-                }
-                for (int p = 0; p < NP; ++p) {
-                    if (!room(&S.empty[pr.slot], pr.phase ^ 1, it * NP + p >= (uint32_t)g.pairs, &S.full[pr.slot], kPair))
-                        break;
-                    if (lane < 2 * ng)
-                        tma_load_3d(pair_s + pr.slot * kPair + (lane / ng) * kBox + mine * args.box_rows * 128,
-                                    &maps.pages, &S.full[pr.slot], p * 128 + (lane / ng) * 64, row, px);
-                    pr.next(g.pairs);
-                }
-                if (a.Ds && room(&S.sempty[sr.slot], sr.phase ^ 1, it >= (uint32_t)g.shared, &S.sfull[sr.slot], kBox)) {
-                    if (lane < ng)
-                        tma_load_3d(shared_s + sr.slot * kBox + lane * args.box_rows * 128, &maps.pages,
-                                    &S.sfull[sr.slot], a.Dl, row, px);
-                    sr.next(g.shared);
-                }
-            }
-        }
-        if (S.abort && lane == 0) {
-            // copies in flight land before the CTA leaves: the last phase of every slot that was filled
-            // (one that never was counts as complete)
-            const uint64_t t0 = Waiter::now();
-            for (int i = 0; i < g.pairs; ++i) w.drain(&S.full[i], (i < pr.slot ? pr.phase : pr.phase ^ 1), t0);
-            for (int i = 0; i < g.shared; ++i) w.drain(&S.sfull[i], (i < sr.slot ? sr.phase : sr.phase ^ 1), t0);
-            if (seg > 0) w.drain(&S.q_full, (seg - 1) & 1, t0);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMAs
-        if (lane == 0) {
-            RingPos qk_p, qk_s, pv_p;
-            constexpr uint32_t idS = idesc_bf16(kTok, NT, 0, 0), idO = idesc_bf16(128, NT, 1, 0);
-            const uint32_t qa = smem_u32(q_s), pa = smem_u32(p_s), ca = smem_u32(pair_s), sa = smem_u32(shared_s);
-            Walk ahead = walk;                    // the scores run one tile ahead
-            bool more = ahead.next(a);
-            int at = more ? ahead.t0 : 0;
-            uint32_t qk_seg = 0, pv_seg = 0, it = 0, qk_it = 0;
-            auto scores = [&]() {
-                // S^T of tile `at` of the segment `ahead`
-                bool ok = at != ahead.t0 || w.wait(&S.q_full, qk_seg & 1);
-                const uint32_t d = t_s + (qk_it & 1) * NT;
-                uint32_t acc = 0;
-                tc_fence_after();
-                for (int p = 0; p < NP; ++p) {
-                    ok = w.wait(&S.full[qk_p.slot], qk_p.phase) && ok;
-                    if (ok && !S.abort) {
+                    for (int n = 0; n < NS; ++n) {
+                        // The shared columns come with the tile's last slot; theirs is free once the scores that
+                        // read it last are done.
+                        const bool with = n == NS - 1 && a.Ds;
+                        if (with && it >= (uint32_t)g.shared)
+                            go = go && w.wait(&S.s_full[(it - g.shared) & 1], ((it - g.shared) >> 1) & 1);
+                        if (it * NS + n >= (uint32_t)g.slots) go = go && w.wait(&S.empty[pr.slot], pr.phase ^ 1);
+                        if (!go) break;
+                        uint64_t *full = &S.full[pr.slot];
+                        mbar_arrive_expect_tx(full, g.sp * kPair + (with ? kBox : 0));
+                        uint8_t *dst = pair_s + pr.slot * g.sp * kPair;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            mma_bf16(d, smem_desc(ca + qk_p.slot * kPair + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kSw128),
-                                     smem_desc(qa + (2 * p + (k >> 2)) * NT * 128 + (k & 3) * 32, 16, 1024, kSw128), idS, acc);
-                            acc = 1;
+                        for (int i = 0; i < 4; ++i) {
+                            if (i >= ng) continue;
+                            for (int x = 0; x < 2 * g.sp; x += args.chunks)
+                                tma_load_4d(dst + x * kBox + i * args.box_rows * 128, &maps.pages, full, 0, row[i],
+                                            n * 2 * g.sp + x, page[i]);
+                            if (with)
+                                tma_load_4d(shared_s + sr * kBox + i * args.box_rows * 128, &maps.pages_shared, full, 0,
+                                            row[i], a.Dl / 64, page[i]);
+                        }
+                        if (with && ++sr == g.shared) sr = 0;
+                        pr.next(g.slots);
+                        if (n == 0 && t == walk.t0) {
+                            // the segment's queries, once the scores of the one before are done
+                            go = seg == 0 || w.wait(&S.q_empty, (seg - 1) & 1);
+                            if (!go) break;
+                            mbar_arrive_expect_tx(&S.q_full, NB * NT * 128);
+                            const int r = walk.seq * R + row0;
+                            for (int c = 0; c < a.Dl / 64; ++c)
+                                tma_load_3d(q_s + c * NT * 128, &maps.q, &S.q_full, c * 64, r, 0);
+                            if (a.Ds) tma_load_3d(q_s + (NB - 1) * NT * 128, &maps.q_shared, &S.q_full, 0, r, 0);
+                            ++seg;
                         }
                     }
-                    qk_p.next(g.pairs);
                 }
-                if (a.Ds) {
-                    ok = w.wait(&S.sfull[qk_s.slot], qk_s.phase) && ok;
-                    if (ok && !S.abort) {
+                walk = after;
+                more = another;
+            }
+            if (S.abort) {
+                // copies in flight land before the CTA leaves: the last phase of every slot that was filled
+                // (one that never was counts as complete)
+                const uint64_t t0 = Waiter::now();
+                for (int i = 0; i < g.slots; ++i) w.drain(&S.full[i], (i < pr.slot ? pr.phase : pr.phase ^ 1), t0);
+                if (seg > 0) w.drain(&S.q_full, (seg - 1) & 1, t0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        if (elect_one()) {
+            RingPos qk_p, pv_p;
+            int qk_s = 0;
+            constexpr uint32_t idS = idesc_bf16(kTok, NT, 0, 0), idO = idesc_bf16(128, NT, 1, 0);
+            // descriptors count in units of 16 bytes: offsets are added to the first slot's
+            const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024, kSw128), dp = smem_desc(smem_u32(p_s), 16, 1024, kSw128);
+            const uint64_t dc = smem_desc(smem_u32(pair_s), 16, 1024, kSw128);
+            const uint64_t dv = smem_desc(smem_u32(pair_s), kBox, 1024, kSw128);
+            const uint64_t ds = smem_desc(smem_u32(shared_s), 16, 1024, kSw128);
+            constexpr uint32_t kQBox = NT * 8, kPairD = kPair / 16, kBoxD = kBox / 16;
+            const uint32_t slot_d = g.sp * kPairD;
+            Walk ahead = walk;                    // the scores run one tile ahead
+            bool more = ahead.next(a), owed = false;
+            int at = more ? ahead.t0 : 0, t = 0;
+            uint32_t qk_seg = 0, pv_seg = 0, it = 0, qk_it = 0;
+            // O^T += L^T P^T of tile t, once P is there
+            auto values = [&](bool ok) {
+                if (t == walk.t0 && pv_seg > 0) ok = w.wait(&S.o_empty, (pv_seg - 1) & 1) && ok;
+                tc_fence_after();
+                for (int n = 0; n < NS; ++n) {
+                    if (ok) {
+                        for (int p = 0; p < g.sp; ++p)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(d, smem_desc(sa + qk_s.slot * kBox + k * 32, 16, 1024, kSw128),
-                                     smem_desc(qa + 2 * NP * NT * 128 + k * 32, 16, 1024, kSw128), idS, 1);
-                        mma_commit(&S.sempty[qk_s.slot]);
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16(t_o + (n * g.sp + p) * NT, dv + (pv_p.slot * slot_d + p * kPairD + k * 128),
+                                         dp + k * 2, idO, t != walk.t0 || k > 0);
+                        mma_commit(&S.empty[pv_p.slot]);
                     }
-                    qk_s.next(g.shared);
+                    pv_p.next(g.slots);
                 }
+                mma_commit(&S.pv_done);
+                owed = false;
+            };
+            // Waits for operands of the next tile's scores; this tile's values go out in the meantime as soon
+            // as softmax is done, so that their slots are free again early.
+            auto arrived = [&](uint64_t *bar, uint32_t parity) {
+                if (mbar_test(bar, parity)) return true;
+                while (owed && !S.abort) {
+                    if (mbar_test(&S.p_ready, it & 1)) values(true);
+                    if (mbar_test(bar, parity)) return true;
+                }
+                return w.wait(bar, parity);
+            };
+            auto scores = [&]() {
+                // S^T of tile `at` of the segment `ahead`
+                bool ok = at != ahead.t0 || arrived(&S.q_full, qk_seg & 1);
+                const uint32_t d = t_s + (qk_it & 1) * NT;
+                uint32_t acc = 0;
+                for (int n = 0; n < NS; ++n) {
+                    ok = arrived(&S.full[qk_p.slot], qk_p.phase) && ok;
+                    tc_fence_after();
+                    if (ok) {
+                        for (int p = 0; p < g.sp; ++p) {
+                            const uint64_t da = dc + (qk_p.slot * slot_d + p * kPairD), db = dq + (n * g.sp + p) * 2 * kQBox;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                mma_bf16(d, da + ((k >> 2) * kBoxD + (k & 3) * 2), db + ((k >> 2) * kQBox + (k & 3) * 2), idS, acc);
+                                acc = 1;
+                            }
+                        }
+                        if (n == NS - 1 && a.Ds)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16(d, ds + (qk_s * kBoxD + k * 2), dq + (2 * NP * kQBox + k * 2), idS, 1);
+                    }
+                    qk_p.next(g.slots);
+                }
+                if (++qk_s == g.shared) qk_s = 0;
                 mma_commit(&S.s_full[qk_it & 1]);
                 ++qk_it;
                 if (++at == ahead.t1) {
@@ -346,22 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
             };
             if (more) scores();
             while (walk.next(a)) {
-                for (int t = walk.t0; t < walk.t1; ++t, ++it) {
+                for (t = walk.t0; t < walk.t1; ++t, ++it) {
+                    owed = true;
                     if (more) scores();
-                    bool ok = w.wait(&S.p_ready, it & 1);
-                    if (t == walk.t0 && pv_seg > 0) ok = w.wait(&S.o_empty, (pv_seg - 1) & 1) && ok;
-                    tc_fence_after();
-                    for (int p = 0; p < NP; ++p) {
-                        if (ok && !S.abort) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16(t_o + p * NT, smem_desc(ca + pv_p.slot * kPair + k * 2048, kBox, 1024, kSw128),
-                                         smem_desc(pa + k * 32, 16, 1024, kSw128), idO, t != walk.t0 || k > 0);
-                            mma_commit(&S.empty[pv_p.slot]);
-                        }
-                        pv_p.next(g.pairs);
-                    }
-                    mma_commit(&S.pv_done);
+                    if (owed) values(w.wait(&S.p_ready, it & 1));
                 }
                 ++pv_seg;
             }
@@ -371,214 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        const int quad = warp & 3;                       // tokens 16 quad .. + 15 of a tile
-        const int tok = lane >> 2, col = 2 * (lane & 3); // my tokens: tok, tok + 8; my columns: 8 c + col, + 1
-        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        const float sc = a.scale * kLog2e;
-        constexpr int C = NT / 8;
-        uint32_t it = 0;
-        const Parts parts = parts_of(a.part, g, a.Dl);
-        bool first_segment = true;
-        while (walk.next(a)) {
-            float m[C][2], l[C][2];
-            int last[C][2];                              // last token that my columns see
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    m[c][u] = -INFINITY;
-                    l[c][u] = 0.f;
-                    const int r = 8 * c + col + u;
-                    last[c][u] = r < rows ? walk.len - a.T + (row0 + r) / a.H : -1;
-                }
-            const int all_see = rows > 0 ? walk.len - a.T + row0 / a.H : -1;     // what every row sees
-            for (int t = walk.t0; t < walk.t1; ++t, ++it) {
-                w.wait(&S.s_full[it & 1], (it >> 1) & 1);
-                tc_fence_after();
-                float v[C][4];
-#pragma unroll
-                for (int c = 0; c < C; c += 2) tmem_ld_16x256b_x2(t_s + (it & 1) * NT + 8 * c + lanes, &v[c][0]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) v[c][u] *= sc;       // log2 units; sc may be negative
-                const uint64_t valid = S.info[it % kInfo];
-                const int j0 = t * kTok + 16 * quad + tok;
-                const bool whole = valid == ~0ull && t * kTok + kTok - 1 <= all_see;
-                if (!whole) {
-                    const bool v0 = valid >> (16 * quad + tok) & 1, v1 = valid >> (16 * quad + tok + 8) & 1;
-#pragma unroll
-                    for (int c = 0; c < C; ++c)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            if (!v0 || j0 > last[c][u]) v[c][u] = -INFINITY;
-                            if (!v1 || j0 + 8 > last[c][u]) v[c][2 + u] = -INFINITY;
-                        }
-                    // rows behind the sequence's end in a page may hold anything: 0 x NaN must not reach O
-                    const int left = walk.len - t * kTok;
-                    if (left < kTok) {
-                        const int end = min(kTok, (max(left, 0) + args.box_rows - 1) / args.box_rows * args.box_rows);
-                        for (int e = tid - 64; e < (end - max(left, 0)) * 8 * 2 * NP; e += 128) {
-                            const int r = max(left, 0) + e / (16 * NP), x = e % (16 * NP);
-                            const int slot = (int)(((long long)it * NP + (x >> 4)) % g.pairs);
-                            *reinterpret_cast<uint4 *>(pair_s + slot * kPair + ((x >> 3) & 1) * kBox + sw128(r, x & 7)) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                }
-                // the tile's maximum of each of my columns
-                float top[C][2];
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float x = fmaxf(v[c][u], v[c][2 + u]);
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        top[c][u] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    }
-                if (lane < 4)
-#pragma unroll
-                    for (int c = 0; c < C; ++c)
-                        *reinterpret_cast<float2 *>(&S.wmax[it & 1][quad][8 * c + col]) = make_float2(top[c][0], top[c][1]);
-                named_bar_sync(1, 128);
-                bool grown = false;
-                float f[C][2];
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    float2 x[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<float2 *>(&S.wmax[it & 1][q][8 * c + col]);
-                    top[c][0] = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
-                    top[c][1] = fmaxf(fmaxf(x[0].y, x[1].y), fmaxf(x[2].y, x[3].y));
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float now = top[c][u];
-                        f[c][u] = 1.f;
-                        if (now > m[c][u] + kGrow || (m[c][u] == -INFINITY && now > -INFINITY)) {
-                            f[c][u] = ex2(m[c][u] - now);
-                            m[c][u] = now;
-                            grown = true;
-                        }
-                    }
-                }
-                const bool rescale = __any_sync(0xffffffffu, grown) && t != walk.t0;
-                // P^T, and my part of the sums
-                uint32_t pk[C][2];
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    float p[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) p[u] = m[c][u & 1] == -INFINITY ? 0.f : ex2(v[c][u] - m[c][u & 1]);
-                    l[c][0] = fmaf(l[c][0], f[c][0], p[0] + p[2]);
-                    l[c][1] = fmaf(l[c][1], f[c][1], p[1] + p[3]);
-                    pk[c][0] = pack2(p[0], p[1]);
-                    pk[c][1] = pack2(p[2], p[3]);
-                }
-                if (it > 0) w.wait(&S.pv_done, (it - 1) & 1);       // P and O^T are free
-                tc_fence_after();
-                if (rescale) {
-                    if (quad == 0 && lane < 4)
-#pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            S.factor[8 * c + col] = f[c][0];
-                            S.factor[8 * c + col + 1] = f[c][1];
-                        }
-                    named_bar_sync(2, 128);
-                    for (int p = 0; p < NP; ++p)
-#pragma unroll
-                        for (int c = 0; c < NT; c += 16) {
-                            float x[16];
-                            tmem_ld16(t_o + p * NT + c + lanes, x);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) x[i] *= S.factor[c + i];
-                            tmem_st16f(t_o + p * NT + c + lanes, x);
-                        }
-                    tmem_wait_st();
-                    named_bar_sync(2, 128);                          // factors read by all
-                }
-#pragma unroll
-                for (int c = 0; c < C; c += 2) {
-                    // matrices: (block c, tokens 0-7), (c, 8-15), (c + 1, 0-7), (c + 1, 8-15) of my warp's 16
-                    const int r = 8 * (c + (lane >> 4)) + (lane & 7), ch = 2 * quad + ((lane >> 3) & 1);
-                    stsm_x4_t(smem_u32(p_s) + sw128(r, ch), pk[c][0], pk[c][1], pk[c + 1][0], pk[c + 1][1]);
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                mbar_arrive(&S.p_ready);
-            }
-            // the segment's result: whole, or one part of a sequence
-            const bool done = walk.t0 == 0 && walk.t1 == walk.tiles;
-            const size_t slot = ((size_t)grp * g.rt + rt) * 2 + (first_segment ? 0 : 1);
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float x = l[c][u];
-                    x += __shfl_xor_sync(0xffffffffu, x, 4);
-                    x += __shfl_xor_sync(0xffffffffu, x, 8);
-                    x += __shfl_xor_sync(0xffffffffu, x, 16);
-                    if (lane < 4) S.lsum[quad][8 * c + col + u] = x;
-                }
-            named_bar_sync(1, 128);
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int r = 8 * c + col + u;
-                    const float x = (S.lsum[0][r] + S.lsum[1][r]) + (S.lsum[2][r] + S.lsum[3][r]);
-                    if (quad == 0 && lane < 4) {
-                        S.factor[r] = x > 0.f ? 1.f / x : 0.f;
-                        const float lse = x > 0.f ? (m[c][u] + lg2(x)) * kLn2 : -INFINITY;
-                        if (r < rows) {
-                            if (!done) parts.lse[slot * NT + r] = lse;
-                            else if (a.lse) a.lse[(size_t)walk.seq * R + row0 + r] = lse;
-                        }
-                    }
-                }
-            w.wait(&S.pv_done, (it - 1) & 1);
-            tc_fence_after();
-            named_bar_sync(1, 128);
-            for (int p = 0; p < NP; ++p) {
-                const int d = p * 128 + 32 * quad + lane;
-#pragma unroll
-                for (int c = 0; c < NT; c += 16) {
-                    float x[16];
-                    tmem_ld16(t_o + p * NT + c + lanes, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = c + i;
-                        if (r >= rows) continue;
-                        const float y = x[i] * S.factor[r];
-                        if (!done) parts.o[(slot * NT + r) * a.Dl + d] = y;
-                        else
-                            static_cast<__nv_bfloat16 *>(a.out)[((size_t)walk.seq * R + row0 + r) * a.Dl + d] =
-                                __float2bfloat16_rn(y);
-                    }
-                }
-            }
-            tc_fence_before();
-            mbar_arrive(&S.o_empty);
-            named_bar_sync(1, 128);                                  // factors are free again
-            if (rt == 0 && tid == 64 && walk.pos >= hi) {
-                // this group's last segment: does its sequence begin here and go on in others?
-                int4 rec = make_int4(-1, 0, 0, 0);
-                if (!done && walk.t0 == 0) {
-                    const long long groups = min((long long)g.groups, total);
-                    const long long end = hi - walk.t1 + walk.tiles - 1;      // the sequence's last tile
-                    long long gl = min(groups - 1, end * groups / total);     // the group that holds it
-                    while (gl + 1 < groups && total * (gl + 1) / groups <= end) ++gl;
-                    while (total * gl / groups > end) --gl;
-                    rec = make_int4(walk.seq, (int)gl, first_segment ? 0 : 1, 0);
-                }
-                parts.rec[grp] = rec;
-            }
-            first_segment = false;
-        }
-        if (rt == 0 && tid == 64 && lo >= hi) parts.rec[grp] = make_int4(-1, 0, 0, 0);
+        const SoftmaxCtx<NT> x{S, args, walk, w, pair_s, p_s, tmem, rt, grp, rows, row0, hi, total};
+        if (warp < 6) softmax<NT, split_cols(NT)>(x, 0);
+        else if constexpr (NT > 16) softmax<NT, NT - split_cols(NT)>(x, 1);
+        if (rt == 0 && tid == 64 && lo >= hi) parts_of(a.part, g, a.Dl).rec[grp] = make_int4(-1, 0, 0, 0);
     }
     tc_fence_before();
     __syncthreads();
@@ -589,61 +682,61 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 }
 
 // Joins the parts of the sequence that begins in group blockIdx.x and goes on in
-// others: out = sum_i e^{lse_i - lse} o_i.  One CTA per row; four quarters of
-// the CTA take every fourth part.
+// others: out = sum_i e^{lse_i - lse} o_i.  128 threads per row and share of the
+// parts: SHARES = 4 takes a row per CTA, each quarter of it every fourth part;
+// SHARES = 1 takes four rows per CTA.
 constexpr int kJoin = 512;
-__global__ void __launch_bounds__(kJoin) latent_join_bf16_kernel(const Args args) {
-    __shared__ float4 acc_s[3][128];
-    __shared__ float w_s[kCtas];
+template <int SHARES> __global__ void __launch_bounds__(kJoin) latent_join_bf16_kernel(const Args args) {
+    __shared__ float4 acc_s[SHARES][128];
     const LatentDecodeArgs &a = args.a;
     const Geometry &g = args.g;
     const Parts parts = parts_of(a.part, g, a.Dl);
-    const int grp = blockIdx.x, rt = blockIdx.y / g.rows, r = blockIdx.y % g.rows, R = a.T * a.H;
-    const int tid = threadIdx.x, lane = tid & 31, part = tid >> 7, c = (tid & 127) * 4;
-    if (rt * g.rows + r >= R) return;
+    const int tid = threadIdx.x, lane = tid & 31, group = tid >> 7, c = (tid & 127) * 4;
+    const int share = SHARES == 4 ? group : 0;
+    const int grp = blockIdx.x, at = SHARES == 4 ? blockIdx.y : blockIdx.y * 4 + group;     // row, by tile
+    const int rt = at / g.rows, r = at % g.rows, R = a.T * a.H;
+    const bool on = at < g.rt * g.rows && rt * g.rows + r < R;
     pdl_wait_primary();
     const int4 rec = parts.rec[grp];
-    if (rec.x < 0) return;
+    if (rec.x < 0 || !on) return;
     const int n = rec.y - grp + 1;
     auto slot = [&](int i) { return (((size_t)(grp + i) * g.rt + rt) * 2 + (i == 0 ? rec.z : 0)) * g.nt + r; };
-    // weights: every warp computes the common maximum and sum
+    // every warp computes the common maximum and sum
     float top = -INFINITY;
     for (int i = lane; i < n; i += 32) top = fmaxf(top, parts.lse[slot(i)]);
 #pragma unroll
     for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    for (int i = lane; i < n; i += 32) {
-        const float x = expf(parts.lse[slot(i)] - base);
-        sum += x;
-        if (tid < 32) w_s[i] = x;
-    }
+    for (int i = lane; i < n; i += 32) sum += expf(parts.lse[slot(i)] - base);
 #pragma unroll
     for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    __syncthreads();
     const float f = sum > 0.f ? 1.f / sum : 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < a.Dl) {
 #pragma unroll 4
-        for (int i = part; i < n; i += 4) {
-            const float4 y = *reinterpret_cast<const float4 *>(parts.o + slot(i) * a.Dl + c);
-            const float wi = w_s[i] * f;
+        for (int i = share; i < n; i += SHARES) {
+            const size_t s = slot(i);
+            const float4 y = *reinterpret_cast<const float4 *>(parts.o + s * a.Dl + c);
+            const float wi = expf(parts.lse[s] - base) * f;
             x.x = fmaf(wi, y.x, x.x), x.y = fmaf(wi, y.y, x.y), x.z = fmaf(wi, y.z, x.z), x.w = fmaf(wi, y.w, x.w);
         }
     }
-    if (part) acc_s[part - 1][tid & 127] = x;
-    __syncthreads();
-    const size_t row = (size_t)rec.x * R + rt * g.rows + r;
-    if (part == 0 && c < a.Dl) {
+    if (SHARES == 4) {
+        acc_s[share][tid & 127] = x;
+        __syncthreads();
+        if (share) return;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const float4 y = acc_s[i][tid];
+        for (int i = 1; i < 4; ++i) {
+            const float4 y = acc_s[i % SHARES][tid];
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
-        uint2 h = make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * a.Dl + c) = h;
     }
-    if (tid == 0 && a.lse) a.lse[row] = sum > 0.f ? base + logf(sum) : -INFINITY;
+    const size_t row = (size_t)rec.x * R + rt * g.rows + r;
+    if (c < a.Dl)
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * a.Dl + c) =
+            make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
+    if ((tid & 127) == 0 && a.lse) a.lse[row] = sum > 0.f ? base + logf(sum) : -INFINITY;
 }
 
 template <int NT> uint32_t small_bytes() { return (uint32_t)sizeof(Small<NT>); }
@@ -658,12 +751,15 @@ Geometry geometry(int T, int H, int Dl, int Ds) {
     const uint32_t small = g.nt == 16 ? small_bytes<16>() : g.nt == 32 ? small_bytes<32>() : g.nt == 48 ? small_bytes<48>() : small_bytes<64>();
     const uint32_t most = 232448 - 1024 - small;
     const int D = Dl + Ds, NP = Dl / 128;
+    // slots of two pairs where the latents have an even number: half the waits for the issuing thread
+    g.sp = NP % 2 == 0 ? 2 : 1;
     // the scores run a tile ahead of the values: two tiles of latents at least; one slot for the
     // shared columns if two do not fit beside them
-    g.shared = Ds ? 2 : 0;
+    g.shared = Ds ? 2 : 1;
     if (Ds && operand_bytes(g.nt, D, 2 * NP, 2) > most) g.shared = 1;
-    g.pairs = std::min<int>(kMaxPairs, (int)((most - operand_bytes(g.nt, D, 0, g.shared)) / kPair));
-    g.smem = operand_bytes(g.nt, D, g.pairs, g.shared) + small + 1024;
+    const uint32_t beside = operand_bytes(g.nt, D, 0, Ds ? g.shared : 0);
+    g.slots = std::min<int>(kMaxSlots, (int)((most - beside) / (g.sp * kPair)));
+    g.smem = beside + g.slots * g.sp * kPair + small + 1024;
     return g;
 }
 static_assert(sizeof(Small<64>) % 8 == 0, "barriers are 8-byte aligned");
@@ -671,7 +767,7 @@ static_assert(sizeof(Small<64>) % 8 == 0, "barriers are 8-byte aligned");
 template <int NT> cudaError_t launch(const Maps &maps, const Args &args, cudaStream_t s) {
     cudaError_t e = allow_smem<latent_decode_kernel<NT>>(232448);
     if (e != cudaSuccess) return e;
-    latent_decode_kernel<NT><<<args.g.rt * args.g.groups, kThreads, args.g.smem, s>>>(maps, args);
+    latent_decode_kernel<NT><<<args.g.rt * args.g.groups, 64 + 32 * softmax_warps(NT), args.g.smem, s>>>(maps, args);
     return cudaGetLastError();
 }
 
@@ -688,14 +784,17 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s) {
     args.g = geometry(a.T, a.H, a.Dl, a.Ds);
     args.box_rows = std::min(kTok, a.page_size & -a.page_size);
     const int D = a.Dl + a.Ds, R = a.T * a.H;
-    if (args.g.pairs < 2 * (a.Dl / 128)) return cudaErrorInvalidConfiguration;
+    if (args.g.slots * args.g.sp < 2 * (a.Dl / 128)) return cudaErrorInvalidConfiguration;
     Maps maps;
     std::memset(&maps, 0, sizeof(maps));
     // without a page the map is never read inside its bounds; any aligned base will do
     const int pages = std::max(1, a.num_pages);
     args.pages_bound = pages;
-    if (!make_map_3d(&maps.pages, a.num_pages ? a.pages : a.q, D, a.page_size, pages, D, (uint64_t)a.page_size * D,
-                     args.box_rows, 1) ||
+    const void *base = a.num_pages ? a.pages : a.q;
+    // one copy brings all chunks of a row box where it fills a tile's rows; smem keeps [chunk][row][64]
+    args.chunks = args.box_rows == kTok ? 2 * args.g.sp : 1;
+    if (!make_map_pages(&maps.pages, base, D, a.page_size, pages, args.box_rows, args.chunks) ||
+        !make_map_pages(&maps.pages_shared, base, D, a.page_size, pages, args.box_rows, 1) ||
         !make_map_3d(&maps.q, a.q, a.Dl, (uint64_t)a.B * R, 1, a.Dl, (uint64_t)a.B * R * a.Dl, args.g.nt, 1) ||
         (a.Ds && !make_map_3d(&maps.q_shared, a.q_shared, a.Ds, (uint64_t)a.B * R, 1, a.Ds, (uint64_t)a.B * R * a.Ds,
                               args.g.nt, 1)))
@@ -709,7 +808,10 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s) {
     }
     if (e != cudaSuccess || args.g.groups == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(args.g.groups, args.g.rt * args.g.rows);
+    // Parts per sequence: about groups / B.  From 16 on a whole CTA per row pays (the parts are read in turn).
+    const bool many = args.g.groups >= 16 * a.B;
+    const int at = args.g.rt * args.g.rows;
+    cfg.gridDim = dim3(args.g.groups, many ? at : (at + 3) / 4);
     cfg.blockDim = dim3(kJoin);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -717,7 +819,8 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_join_bf16_kernel, args);
+    return many ? cudaLaunchKernelEx(&cfg, latent_join_bf16_kernel<4>, args)
+                : cudaLaunchKernelEx(&cfg, latent_join_bf16_kernel<1>, args);
 }
 
 }  // namespace rda

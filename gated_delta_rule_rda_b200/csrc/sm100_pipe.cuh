@@ -12,9 +12,9 @@ namespace ptx {
 
 // Bounded mbarrier waits of one CTA.  `abort` is a word of shared memory: a
 // wait that runs out records RDA_ERR_TIMEOUT in *err and sets it; from then on
-// every wait of the CTA returns at once.  All threads run their loops to the
-// end either way (no thread leaves a named barrier short); MMAs and copies are
-// issued only while `ok` holds.
+// every wait of the CTA that would block returns at once.  All threads run their
+// loops to the end either way (no thread leaves a named barrier short); MMAs and
+// copies are issued only after waits that succeeded.
 struct Waiter {
     volatile int *abort;
     int32_t *err;
@@ -47,6 +47,38 @@ struct Waiter {
             if (now() - t0 > limit_ns) return;
     }
 };
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// One lane of a converged warp.  The MMA issuers branch on it (and not on the
+// lane's number): the compiler then knows that one thread runs the branch and
+// keeps descriptors in uniform registers.  An unrolled chain of M = 64, N = 16
+// products issues every 24 cycles this way, every 51 behind `lane == 0`.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 
 // A slot of a ring and the parity of its next phase.
 struct RingPos {
@@ -145,5 +177,9 @@ __device__ __forceinline__ uint8_t *align_1024(uint8_t *raw) { return raw + ((10
 // TMA map with boxes of 64 x box1 x box2, 128-byte swizzle, zeros outside.
 bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                  uint64_t stride2, uint32_t box1, uint32_t box2);
+// Rows of `cols` bf16 values in pages, as [page][column / 64][row][64]: boxes of `box_rows` rows x `chunks` times 64
+// columns land as `chunks` tiles of 128-byte rows.
+bool make_map_pages(CUtensorMap *map, const void *base, uint64_t cols, uint64_t page_size, uint64_t pages,
+                    uint32_t box_rows, uint32_t chunks);
 
 }  // namespace rda
