@@ -75,7 +75,8 @@ rda_status_t rda_latent_prefill(const void *q, const void *q_shared, const void 
     a.out = out; a.lse = lse;
     a.err = static_cast<int32_t *>(workspace);
     a.wait_ns = wait_settings().wait_ns;
-    return done(launch_latent_forward_f32(a, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return done(dtype == RDA_BF16 ? launch_latent_forward_tc(a, s) : launch_latent_forward_f32(a, s));
 }
 
 size_t rda_latent_backward_workspace_bytes(int total_q, int total_k, int H, int Dk, int Ds, int Dv, int num_seqs) {

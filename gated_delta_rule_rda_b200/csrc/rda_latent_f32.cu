@@ -586,8 +586,7 @@ template <typename T> cudaError_t decode_t(const LatentDecodeArgs &a, cudaStream
 }  // namespace
 
 cudaError_t launch_latent_forward_f32(const LatentArgs &a, cudaStream_t s) {
-    if (a.dtype == RDA_F32) return a.Dv == 64 ? forward_nv<float, 1>(a, s) : forward_nv<float, 2>(a, s);
-    return a.Dv == 64 ? forward_nv<__nv_bfloat16, 1>(a, s) : forward_nv<__nv_bfloat16, 2>(a, s);
+    return a.Dv == 64 ? forward_nv<float, 1>(a, s) : forward_nv<float, 2>(a, s);
 }
 
 cudaError_t launch_latent_delta(const LatentArgs &a, cudaStream_t s) {

@@ -28,6 +28,10 @@ bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, u
     return encode_bf16(map, base, 3, dims, strides, box);
 }
 
+bool make_map_heads(CUtensorMap *map, const void *base, int D, int H, long rows, uint32_t box, const void *any) {
+    return make_map_3d(map, rows ? base : any, D, H, rows ? rows : 1, D, (uint64_t)H * D, 1, box);
+}
+
 bool make_map_pages(CUtensorMap *map, const void *base, uint64_t cols, uint64_t page_size, uint64_t pages,
                     uint32_t box_rows, uint32_t chunks) {
     const cuuint64_t dims[4] = {64, page_size, cols / 64, pages};

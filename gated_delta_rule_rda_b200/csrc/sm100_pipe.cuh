@@ -134,6 +134,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float *v) {
     uint32_t r[16];
 #pragma unroll
@@ -177,6 +182,9 @@ __device__ __forceinline__ uint8_t *align_1024(uint8_t *raw) { return raw + ((10
 // TMA map with boxes of 64 x box1 x box2, 128-byte swizzle, zeros outside.
 bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                  uint64_t stride2, uint32_t box1, uint32_t box2);
+// [rows, H, D]: boxes of 64 columns of one head x `box` rows; where there are no rows the map is only read outside
+// its bounds, and `any` is its base.
+bool make_map_heads(CUtensorMap *map, const void *base, int D, int H, long rows, uint32_t box, const void *any);
 // Rows of `cols` bf16 values in pages, as [page][column / 64][row][64]: boxes of `box_rows` rows x `chunks` times 64
 // columns land as `chunks` tiles of 128-byte rows.
 bool make_map_pages(CUtensorMap *map, const void *base, uint64_t cols, uint64_t page_size, uint64_t pages,
