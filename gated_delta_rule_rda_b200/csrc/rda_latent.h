@@ -104,6 +104,8 @@ cudaError_t launch_latent_delta(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_latent_shared_sum(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s);
 // bf16: tensor cores
+cudaError_t launch_latent_backward_tc(const LatentArgs &a, void *scratch, cudaStream_t s);
+size_t latent_backward_tc_scratch_bytes(int total_q, int total_k, int num_seqs, int H, int Ds);
 cudaError_t launch_latent_forward_tc(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s);

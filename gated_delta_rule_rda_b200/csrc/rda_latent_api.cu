@@ -81,7 +81,8 @@ rda_status_t rda_latent_prefill(const void *q, const void *q_shared, const void 
 
 size_t rda_latent_backward_workspace_bytes(int total_q, int total_k, int H, int Dk, int Ds, int Dv, int num_seqs) {
     if (total_q < 0 || total_k < 0 || H <= 0 || H > kMaxHeads || num_seqs < 0 || !head_dims_ok(Dk, Ds, Dv)) return 0;
-    return kErrorWordBytes + latent_backward_scratch_bytes(total_q, total_k, H, Ds);
+    return kErrorWordBytes + std::max(latent_backward_scratch_bytes(total_q, total_k, H, Ds),
+                                      latent_backward_tc_scratch_bytes(total_q, total_k, num_seqs, H, Ds));
 }
 
 rda_status_t rda_latent_backward(const void *q, const void *q_shared, const void *k, const void *k_shared, const void *v,
@@ -113,9 +114,10 @@ rda_status_t rda_latent_backward(const void *q, const void *q_shared, const void
     a.err = static_cast<int32_t *>(workspace);
     a.wait_ns = wait_settings().wait_ns;
     uint8_t *scratch = static_cast<uint8_t *>(workspace) + kErrorWordBytes;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == RDA_BF16) return done(launch_latent_backward_tc(a, scratch, s));
     a.delta = reinterpret_cast<float *>(scratch);
     a.dks_heads = reinterpret_cast<float *>(scratch + latent_backward_scratch_bytes(total_q, 0, H, Ds));
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_latent_delta(a, s);
     if (e == cudaSuccess) e = launch_latent_backward_f32(a, s);
     if (e == cudaSuccess && Ds) e = launch_latent_shared_sum(a, s);

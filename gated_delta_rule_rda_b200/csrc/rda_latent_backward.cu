@@ -1,0 +1,644 @@
+// Gradients of latent attention in its expanded form (bf16), packed sequences.
+//
+//   p_ij = e^{s_ij - lse_i},  dp_ij = do_i . v_j,  delta_i = do_i . o_i,  ds_ij = p_ij (dp_ij - delta_i)
+//   dv_j = sum_i p_ij do_i,   dk_j = scale sum_i ds_ij q_i,   dq_i = scale sum_j ds_ij k_j
+//
+// Bound by the tensor cores.  Two kernels, each with the sums that its CTA owns
+// in TMEM: one over keys (dv, dk), one over query rows (dq).  The scores and dp
+// are formed in both, seven products instead of five; in exchange no sum is
+// shared between CTAs: nothing depends on the order of atomics, and no fp32
+// copy of dq is written, cleared and converted.
+//
+//   keys    128 keys x 64 query rows a step:  S^T = K Q^T,  dP^T = V dO^T  (shared memory),
+//           then dV += P^T dO and dK += dS^T Q with P^T, dS^T as TMEM operands
+//   rows    128 query rows x 96 keys a step:  S = Q K^T,  dP = dO V^T,  then dQ += dS K
+//
+// In both, one thread issues the MMAs: the next step's scores go out before this
+// step's P is consumed, so that the tensor pipe and the eight element-wise warps
+// (a lane per key, or per query row; two warps share the columns of a lane)
+// work at the same time.  P and dS are rounded to bf16 for their products; p,
+// dp, delta and all sums are fp32.
+//
+// The key part that all heads share gets its gradient from every head: the
+// heads' parts are written in fp32 and summed in a fixed order afterwards.
+#include <cmath>
+#include <cstring>
+
+#include "rda_latent.h"
+#include "sm100_pipe.cuh"
+
+namespace rda {
+namespace {
+
+using namespace ptx;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 64 + 256;
+constexpr uint32_t kCols = 512;
+constexpr int kStat = 64;                       // query rows of a block of statistics
+constexpr uint32_t kBig = 128 * 128;            // 128 rows x 64 columns
+
+// keys kernel
+constexpr int kRows = 64, kStagesA = 3;         // query rows of a step
+constexpr uint32_t kSmall = kRows * 128;        // 64 rows x 64 columns
+constexpr uint32_t kTdV = 0, kTdK = 128, kTS = 320, kTdP = 384, kTP = 448, kTdS = 480;
+// rows kernel
+constexpr int kKeys = 96, kStagesB = 2;         // keys of a step
+constexpr uint32_t kMid = kKeys * 128;          // 96 rows x 64 columns
+constexpr uint32_t kUdQ = 0, kUS = 192, kUdP = 288, kUdS = 384;
+
+struct Maps {
+    CUtensorMap q, q_shared, k, k_shared, v, d_out;
+};
+
+// ---------------------------------------------------------------------------
+// Statistics of 64 query rows of a head, ready for the exponent: lse log2 e and
+// delta, [head][block][2][64].  Rows behind the sequence's end, and rows that
+// saw no key, get +inf: their p is 2^-inf = 0.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) latent_stats_kernel(const LatentArgs a, float *stats) {
+    int t;
+    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, kStat, blockIdx.x, &t);
+    const SeqSpan sq = seq_span(a.cu_q, n, a.total_q);
+    const int h = blockIdx.y, r = threadIdx.x >> 2, part = threadIdx.x & 3, row = t * kStat + r;
+    float x = 0.f;
+    const size_t at = (size_t)(sq.start + row) * a.H + h;
+    if (row < sq.len) {
+        const uint4 *o = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.out) + at * a.Dv);
+        const uint4 *d = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.d_out) + at * a.Dv);
+        uint4 u[4], v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (part + 4 * i < a.Dv / 8) u[i] = o[part + 4 * i], v[i] = d[part + 4 * i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (part + 4 * i < a.Dv / 8) {
+                const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&u[i]);
+                const __nv_bfloat162 *q = reinterpret_cast<const __nv_bfloat162 *>(&v[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = __bfloat1622float2(p[k]), g = __bfloat1622float2(q[k]);
+                    x = fmaf(f.x, g.x, fmaf(f.y, g.y, x));
+                }
+            }
+    }
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    if (part == 0) {
+        float *s = stats + ((size_t)h * gridDim.x + blockIdx.x) * 2 * kStat;
+        const float lse = row < sq.len ? a.lse[at] : -INFINITY;
+        s[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+        s[kStat + r] = row < sq.len ? x : 0.f;
+    }
+}
+
+__device__ __forceinline__ int stat_block(const LatentArgs &a, int n, int row) {
+    return clamped(a.cu_q, n, a.total_q) / kStat + n + row / kStat;
+}
+
+// 16-byte chunks [0, 8) of rows [from, to) of `chunks` tiles of 128-byte rows, zeroed by 256 threads.
+__device__ __forceinline__ void zero_rows(uint8_t *tile, uint32_t tile_bytes, int chunks, int from, int to) {
+    const int n = (to - from) * 8;
+    for (int c = 0; c < chunks; ++c)
+        for (int e = threadIdx.x - 64; e < n; e += 256)
+            *reinterpret_cast<uint4 *>(tile + c * tile_bytes + sw128(from + (e >> 3), e & 7)) = make_uint4(0, 0, 0, 0);
+}
+
+// NC columns of a row of an accumulator (my lane), times f, as bf16 or fp32 to `out`.
+template <typename T>
+__device__ __forceinline__ void store_cols(uint32_t t, int cols, float f, T *out, bool mine, bool zero) {
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+        float x[32];
+        if (zero) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        } else {
+            tmem_ld32(t + c, x);
+            tmem_wait_ld();
+        }
+        if (!mine) continue;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4 *>(out + c + i) = make_uint4(pack2(x[i] * f, x[i + 1] * f), pack2(x[i + 2] * f, x[i + 3] * f),
+                                                                     pack2(x[i + 4] * f, x[i + 5] * f), pack2(x[i + 6] * f, x[i + 7] * f));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(out + c + i) = make_float4(x[i] * f, x[i + 1] * f, x[i + 2] * f, x[i + 3] * f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dK and dV: one CTA per (128 keys, head).
+// ---------------------------------------------------------------------------
+struct BarsA {
+    uint64_t kv_full, q_full[kStagesA], q_empty[kStagesA];
+    uint64_t s_ready, s_free, p_ready, dv_done, dp_ready, dp_free, ds_ready, dk_done;
+    uint32_t tmem;
+    volatile int abort;
+};
+__host__ __device__ inline uint32_t stage_a(int nk, int nv) { return (nk + nv) * kSmall + 1024; }
+inline uint32_t smem_a(int nk, int nv) { return (nk + nv) * kBig + kStagesA * stage_a(nk, nv) + sizeof(BarsA) + 1024; }
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_dkv_kernel(const __grid_constant__ Maps maps, const LatentArgs a, const float *stats, int stat_blocks) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = align_1024(smem_raw);
+    const int nd = a.Dk / 64, nk = (a.Dk + a.Ds) / 64, nv = a.Dv / 64;
+    const uint32_t stage = stage_a(nk, nv);
+    uint8_t *k_s = sm, *v_s = k_s + nk * kBig, *st_s = v_s + nv * kBig;       // a stage: Q, dO, statistics
+    BarsA &B = *reinterpret_cast<BarsA *>(st_s + kStagesA * stage);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Waiter w{&B.abort, a.err, a.wait_ns};
+
+    // heads side by side; the first keys of a sequence (which the most queries see) first
+    const int h = blockIdx.x % a.H;
+    int t;
+    const int n = find_tile(a.cu_k, a.num_seqs, a.total_k, 128, blockIdx.x / a.H, &t);
+    const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
+    const int k0 = t * 128, more = sk.len - sq.len;
+    if (k0 >= sk.len) return;
+    const int first = a.causal ? max(0, k0 - more) / kRows : 0;               // the first step with a query that sees key k0
+    const int steps = max(0, (sq.len + kRows - 1) / kRows - first);
+
+    if (warp == 0) {
+        tmem_alloc(&B.tmem, kCols);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        mbar_init(&B.kv_full, 1);
+        for (int i = 0; i < kStagesA; ++i) mbar_init(&B.q_full[i], 1), mbar_init(&B.q_empty[i], 1);
+        mbar_init(&B.s_ready, 1);
+        mbar_init(&B.dp_ready, 1);
+        mbar_init(&B.dv_done, 1);
+        mbar_init(&B.dk_done, 1);
+        mbar_init(&B.s_free, 256);
+        mbar_init(&B.p_ready, 256);
+        mbar_init(&B.dp_free, 256);
+        mbar_init(&B.ds_ready, 256);
+        B.abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.q);
+        prefetch_tensormap(&maps.d_out);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = B.tmem;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (elect_one() && steps > 0) {
+            mbar_arrive_expect_tx(&B.kv_full, (nk + nv) * kBig);
+            for (int c = 0; c < nk; ++c)
+                tma_load_3d(k_s + c * kBig, c < nd ? &maps.k : &maps.k_shared, &B.kv_full, (c < nd ? c : c - nd) * 64,
+                            c < nd ? h : 0, sk.start + k0);
+            for (int c = 0; c < nv; ++c) tma_load_3d(v_s + c * kBig, &maps.v, &B.kv_full, c * 64, h, sk.start + k0);
+            RingPos p;
+            int loaded = 0;
+            for (; loaded < steps; ++loaded) {
+                const int row = (first + loaded) * kRows;
+                if (loaded >= kStagesA && !w.wait(&B.q_empty[p.slot], p.phase ^ 1)) break;
+                uint8_t *dst = st_s + p.slot * stage;
+                mbar_arrive_expect_tx(&B.q_full[p.slot], (nk + nv) * kSmall + 2 * kStat * 4);
+                for (int c = 0; c < nk; ++c)
+                    tma_load_3d(dst + c * kSmall, c < nd ? &maps.q : &maps.q_shared, &B.q_full[p.slot],
+                                (c < nd ? c : c - nd) * 64, h, sq.start + row);
+                for (int c = 0; c < nv; ++c)
+                    tma_load_3d(dst + (nk + c) * kSmall, &maps.d_out, &B.q_full[p.slot], c * 64, h, sq.start + row);
+                bulk_load(dst + (nk + nv) * kSmall, stats + ((size_t)h * stat_blocks + stat_block(a, n, row)) * 2 * kStat,
+                          2 * kStat * 4, &B.q_full[p.slot]);
+                p.next(kStagesA);
+            }
+            if (B.abort) {
+                const uint64_t t0 = Waiter::now();
+                w.drain(&B.kv_full, 0, t0);
+                for (int i = max(0, loaded - kStagesA); i < loaded; ++i)
+                    w.drain(&B.q_full[i % kStagesA], (i / kStagesA) & 1, t0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        if (elect_one() && steps > 0) {
+            const uint32_t idN64 = idesc_bf16(128, kRows, 0, 0), idV = idesc_bf16(128, a.Dv, 0, 1),
+                           idK = idesc_bf16(128, 64 * nk, 0, 1);
+            const uint64_t dk = smem_desc(smem_u32(k_s), 16, 1024, kSw128), dv = smem_desc(smem_u32(v_s), 16, 1024, kSw128);
+            const uint64_t ds = smem_desc(smem_u32(st_s), 16, 1024, kSw128);          // K-major
+            const uint64_t dm = smem_desc(smem_u32(st_s), kSmall, 1024, kSw128);      // MN-major
+            bool ok = w.wait(&B.kv_full, 0);
+            // S^T or dP^T of step i: `chunks` of 64 columns of the stationary tile against the stage's
+            auto product = [&](uint32_t d, uint64_t da, uint64_t db, int chunks) {
+                for (int c = 0; c < chunks; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(d, da + c * (kBig / 16) + 2 * k, db + c * (kSmall / 16) + 2 * k, idN64, c > 0 || k > 0);
+            };
+            RingPos next, now;
+            ok = w.wait(&B.q_full[0], 0) && ok;
+            tc_fence_after();
+            if (ok) product(tmem + kTS, dk, ds, nk);
+            mma_commit(&B.s_ready);
+            if (ok) product(tmem + kTdP, dv, ds + nk * (kSmall / 16), nv);
+            mma_commit(&B.dp_ready);
+            next.next(kStagesA);
+            for (int i = 0; i < steps; ++i) {
+                const uint64_t off = now.slot * (stage / 16), off_n = next.slot * (stage / 16);
+                if (i + 1 < steps) {
+                    ok = w.wait(&B.q_full[next.slot], next.phase) && ok;
+                    ok = w.wait(&B.s_free, i & 1) && ok;
+                    tc_fence_after();
+                    if (ok) product(tmem + kTS, dk, ds + off_n, nk);
+                    mma_commit(&B.s_ready);
+                }
+                ok = w.wait(&B.p_ready, i & 1) && ok;
+                tc_fence_after();
+                if (ok) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16_ta(tmem + kTdV, tmem + kTP + 8 * k, dm + off + nk * (kSmall / 16) + 128 * k, idV, i > 0 || k > 0);
+                }
+                mma_commit(&B.dv_done);
+                if (i + 1 < steps) {
+                    ok = w.wait(&B.dp_free, i & 1) && ok;
+                    tc_fence_after();
+                    if (ok) product(tmem + kTdP, dv, ds + off_n + nk * (kSmall / 16), nv);
+                    mma_commit(&B.dp_ready);
+                }
+                ok = w.wait(&B.ds_ready, i & 1) && ok;
+                tc_fence_after();
+                if (ok) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16_ta(tmem + kTdK, tmem + kTdS + 8 * k, dm + off + 128 * k, idK, i > 0 || k > 0);
+                }
+                mma_commit(&B.q_empty[now.slot]);
+                mma_commit(&B.dk_done);
+                now.next(kStagesA);
+                next.next(kStagesA);
+            }
+            if (B.abort) w.drain(&B.dk_done, (steps - 1) & 1, Waiter::now());
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ element-wise: my key, half of the query rows
+        const int quad = warp & 3, half = warp >= 6, key = k0 + 32 * quad + lane;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        const uint32_t t_s = tmem + kTS + 32 * half + lanes, t_dp = tmem + kTdP + 32 * half + lanes,
+                       t_p = tmem + kTP + 16 * half + lanes, t_ds = tmem + kTdS + 16 * half + lanes;
+        const float sc = a.scale * kLog2e;
+        RingPos p;
+        for (int i = 0; i < steps; ++i) {
+            const int row0 = (first + i) * kRows;
+            const float *st = reinterpret_cast<const float *>(st_s + p.slot * stage + (nk + nv) * kSmall) + 32 * half;
+            const int rows = sq.len - row0;                        // query rows of this step that exist
+            // my first visible query among my 32
+            const int from = a.causal ? key - more - row0 - 32 * half : 0, to = rows - 32 * half;
+            const bool masked = __any_sync(0xffffffffu, from > 0 || to < 32);
+            float x[32], y[32];
+            w.wait(&B.s_ready, i & 1);
+            tc_fence_after();
+            tmem_ld32(t_s, x);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(&B.s_free);
+            w.wait(&B.q_full[p.slot], p.phase);                    // the statistics, written by the copy
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                const float4 lse = *reinterpret_cast<const float4 *>(st + c);
+                x[c] = ex2(fmaf(x[c], sc, -lse.x));
+                x[c + 1] = ex2(fmaf(x[c + 1], sc, -lse.y));
+                x[c + 2] = ex2(fmaf(x[c + 2], sc, -lse.z));
+                x[c + 3] = ex2(fmaf(x[c + 3], sc, -lse.w));
+            }
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) x[c] = c >= from && c < to ? x[c] : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) pk[c / 2] = pack2(x[c], x[c + 1]);
+            if (i > 0) w.wait(&B.dv_done, (i - 1) & 1);
+            tc_fence_after();
+            tmem_st16(t_p, pk);
+            if (rows < kRows) {
+                // rows behind the sequence may hold anything: 0 x NaN must not reach the sums
+                zero_rows(st_s + p.slot * stage, kSmall, nk + nv, rows, kRows);
+                fence_proxy_async_smem();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&B.p_ready);
+            w.wait(&B.dp_ready, i & 1);
+            tc_fence_after();
+            tmem_ld32(t_dp, y);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(&B.dp_free);
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                const float4 d = *reinterpret_cast<const float4 *>(st + kStat + c);
+                y[c] = x[c] * (y[c] - d.x);
+                y[c + 1] = x[c + 1] * (y[c + 1] - d.y);
+                y[c + 2] = x[c + 2] * (y[c + 2] - d.z);
+                y[c + 3] = x[c + 3] * (y[c + 3] - d.w);
+            }
+            if (rows < kRows) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) y[c] = c < to ? y[c] : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) pk[c / 2] = pack2(y[c], y[c + 1]);
+            if (i > 0) w.wait(&B.dk_done, (i - 1) & 1);
+            tc_fence_after();
+            tmem_st16(t_ds, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&B.ds_ready);
+            p.next(kStagesA);
+        }
+        if (steps > 0) {
+            w.wait(&B.dk_done, (steps - 1) & 1);
+            tc_fence_after();
+        }
+        const bool mine = key < sk.len;
+        const size_t at = (size_t)(sk.start + key) * a.H + h;
+        if (half == 0) {
+            store_cols(tmem + kTdV + lanes, a.Dv, 1.f, static_cast<__nv_bfloat16 *>(a.dv) + at * a.Dv, mine, steps == 0);
+        } else {
+            store_cols(tmem + kTdK + lanes, a.Dk, a.scale, static_cast<__nv_bfloat16 *>(a.dk) + at * a.Dk, mine, steps == 0);
+            if (a.Ds)
+                store_cols(tmem + kTdK + a.Dk + lanes, a.Ds, a.scale, a.dks_heads + at * a.Ds, mine, steps == 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dQ: one CTA per (128 query rows, head).
+// ---------------------------------------------------------------------------
+struct BarsB {
+    uint64_t q_full, kv_full[kStagesB], kv_empty[kStagesB];
+    uint64_t s_ready, s_free, dp_ready, dp_free, ds_ready, dq_done;
+    uint32_t tmem;
+    volatile int abort;
+};
+inline uint32_t smem_b(int nk, int nv) { return (nk + nv) * (kBig + kStagesB * kMid) + sizeof(BarsB) + 1024; }
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_dq_kernel(const __grid_constant__ Maps maps, const LatentArgs a, const float *stats, int stat_blocks) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = align_1024(smem_raw);
+    const int nd = a.Dk / 64, nk = (a.Dk + a.Ds) / 64, nv = a.Dv / 64;
+    const uint32_t stage = (nk + nv) * kMid;
+    uint8_t *q_s = sm, *o_s = q_s + nk * kBig, *st_s = o_s + nv * kBig;       // a stage: K, V
+    BarsB &B = *reinterpret_cast<BarsB *>(st_s + kStagesB * stage);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Waiter w{&B.abort, a.err, a.wait_ns};
+
+    const int h = blockIdx.x % a.H;
+    int t;
+    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, 128, (int)(gridDim.x / a.H - 1 - blockIdx.x / a.H), &t);
+    const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
+    const int r0 = t * 128, more = sk.len - sq.len;
+    const int rows = min(128, sq.len - r0);
+    if (rows <= 0) return;
+    const int end = a.causal ? min(sk.len, r0 + rows + more) : sk.len;
+    const int steps = end > 0 ? (end + kKeys - 1) / kKeys : 0;
+
+    if (warp == 0) {
+        tmem_alloc(&B.tmem, kCols);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        mbar_init(&B.q_full, 1);
+        for (int i = 0; i < kStagesB; ++i) mbar_init(&B.kv_full[i], 1), mbar_init(&B.kv_empty[i], 1);
+        mbar_init(&B.s_ready, 1);
+        mbar_init(&B.dp_ready, 1);
+        mbar_init(&B.dq_done, 1);
+        mbar_init(&B.s_free, 256);
+        mbar_init(&B.dp_free, 256);
+        mbar_init(&B.ds_ready, 256);
+        B.abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.q);
+        prefetch_tensormap(&maps.d_out);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = B.tmem;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (elect_one() && steps > 0) {
+            mbar_arrive_expect_tx(&B.q_full, (nk + nv) * kBig);
+            for (int c = 0; c < nk; ++c)
+                tma_load_3d(q_s + c * kBig, c < nd ? &maps.q : &maps.q_shared, &B.q_full, (c < nd ? c : c - nd) * 64, h,
+                            sq.start + r0);
+            for (int c = 0; c < nv; ++c) tma_load_3d(o_s + c * kBig, &maps.d_out, &B.q_full, c * 64, h, sq.start + r0);
+            RingPos p;
+            int loaded = 0;
+            for (; loaded < steps; ++loaded) {
+                if (loaded >= kStagesB && !w.wait(&B.kv_empty[p.slot], p.phase ^ 1)) break;
+                const int row = sk.start + loaded * kKeys;
+                uint8_t *dst = st_s + p.slot * stage;
+                mbar_arrive_expect_tx(&B.kv_full[p.slot], stage);
+                for (int c = 0; c < nk; ++c)
+                    tma_load_3d(dst + c * kMid, c < nd ? &maps.k : &maps.k_shared, &B.kv_full[p.slot],
+                                (c < nd ? c : c - nd) * 64, c < nd ? h : 0, row);
+                for (int c = 0; c < nv; ++c)
+                    tma_load_3d(dst + (nk + c) * kMid, &maps.v, &B.kv_full[p.slot], c * 64, h, row);
+                p.next(kStagesB);
+            }
+            if (B.abort) {
+                const uint64_t t0 = Waiter::now();
+                w.drain(&B.q_full, 0, t0);
+                for (int i = max(0, loaded - kStagesB); i < loaded; ++i)
+                    w.drain(&B.kv_full[i % kStagesB], (i / kStagesB) & 1, t0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        if (elect_one() && steps > 0) {
+            const uint32_t idN = idesc_bf16(128, kKeys, 0, 0), idQ = idesc_bf16(128, 64 * nk, 0, 1);
+            const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024, kSw128), dO = smem_desc(smem_u32(o_s), 16, 1024, kSw128);
+            const uint64_t ds = smem_desc(smem_u32(st_s), 16, 1024, kSw128), dm = smem_desc(smem_u32(st_s), kMid, 1024, kSw128);
+            bool ok = w.wait(&B.q_full, 0);
+            auto product = [&](uint32_t d, uint64_t da, uint64_t db, int chunks) {
+                for (int c = 0; c < chunks; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(d, da + c * (kBig / 16) + 2 * k, db + c * (kMid / 16) + 2 * k, idN, c > 0 || k > 0);
+            };
+            RingPos next, now;
+            for (int i = -1; i < steps; ++i) {
+                if (i + 1 < steps) {
+                    const uint64_t off = next.slot * (stage / 16);
+                    ok = w.wait(&B.kv_full[next.slot], next.phase) && ok;
+                    if (i >= 0) ok = w.wait(&B.s_free, i & 1) && ok;
+                    tc_fence_after();
+                    if (ok) product(tmem + kUS, dq, ds + off, nk);
+                    mma_commit(&B.s_ready);
+                    if (i >= 0) ok = w.wait(&B.dp_free, i & 1) && ok;
+                    tc_fence_after();
+                    if (ok) product(tmem + kUdP, dO, ds + off + nk * (kMid / 16), nv);
+                    mma_commit(&B.dp_ready);
+                    next.next(kStagesB);
+                }
+                if (i < 0) continue;
+                ok = w.wait(&B.ds_ready, i & 1) && ok;
+                tc_fence_after();
+                if (ok) {
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_bf16_ta(tmem + kUdQ, tmem + kUdS + 8 * k, dm + now.slot * (stage / 16) + 128 * k, idQ, i > 0 || k > 0);
+                }
+                mma_commit(&B.kv_empty[now.slot]);
+                mma_commit(&B.dq_done);
+                now.next(kStagesB);
+            }
+            if (B.abort) w.drain(&B.dq_done, (steps - 1) & 1, Waiter::now());
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ element-wise: my query row, half of the keys
+        constexpr int C = kKeys / 2;
+        const int quad = warp & 3, half = warp >= 6, r = 32 * quad + lane, row = r0 + r;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        const uint32_t t_s = tmem + kUS + C * half + lanes, t_dp = tmem + kUdP + C * half + lanes,
+                       t_ds = tmem + kUdS + C / 2 * half + lanes;
+        const float sc = a.scale * kLog2e;
+        const int limit = r >= rows ? 0 : a.causal ? min(sk.len, row + more + 1) : sk.len;      // keys that my row sees
+        float lse = INFINITY, delta = 0.f;
+        if (r < rows) {
+            const float *st = stats + ((size_t)h * stat_blocks + stat_block(a, n, row)) * 2 * kStat + row % kStat;
+            lse = st[0];
+            delta = st[kStat];
+        }
+        RingPos p;
+        for (int i = 0; i < steps; ++i) {
+            float x[C];
+            uint32_t pk[C / 2];
+            const int left = limit - i * kKeys - C * half;
+            const bool masked = __any_sync(0xffffffffu, left < C);
+            w.wait(&B.s_ready, i & 1);
+            tc_fence_after();
+            tmem_ld32(t_s, x);
+            tmem_ld16(t_s + 32, x + 32);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(&B.s_free);
+#pragma unroll
+            for (int c = 0; c < C; ++c) x[c] = ex2(fmaf(x[c], sc, -lse));
+            const int keys = sk.len - i * kKeys;
+            if (keys < kKeys) {
+                // keys behind the sequence may hold anything: 0 x NaN must not reach the sums
+                w.wait(&B.kv_full[p.slot], p.phase);
+                zero_rows(st_s + p.slot * stage, kMid, nk, keys, kKeys);
+                fence_proxy_async_smem();
+            }
+            w.wait(&B.dp_ready, i & 1);
+            tc_fence_after();
+            float y[C];
+            tmem_ld32(t_dp, y);
+            tmem_ld16(t_dp + 32, y + 32);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(&B.dp_free);
+#pragma unroll
+            for (int c = 0; c < C; ++c) x[c] *= y[c] - delta;
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) x[c] = c < left ? x[c] : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < C; c += 2) pk[c / 2] = pack2(x[c], x[c + 1]);
+            if (i > 0) w.wait(&B.dq_done, (i - 1) & 1);
+            tc_fence_after();
+            tmem_st16(t_ds, pk);
+            tmem_st8(t_ds + 16, pk + 16);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&B.ds_ready);
+            p.next(kStagesB);
+        }
+        if (steps > 0) {
+            w.wait(&B.dq_done, (steps - 1) & 1);
+            tc_fence_after();
+        }
+        const size_t at = (size_t)(sq.start + row) * a.H + h;
+        const bool mine = r < rows;
+        // the columns in halves: Dk / 2 and Ds / 2 each
+        store_cols(tmem + kUdQ + half * (a.Dk / 2) + lanes, a.Dk / 2, a.scale,
+                   static_cast<__nv_bfloat16 *>(a.dq) + at * a.Dk + half * (a.Dk / 2), mine, steps == 0);
+        if (a.Ds)
+            store_cols(tmem + kUdQ + a.Dk + half * (a.Ds / 2) + lanes, a.Ds / 2, a.scale,
+                       static_cast<__nv_bfloat16 *>(a.dq_shared) + at * a.Ds + half * (a.Ds / 2), mine, steps == 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+size_t stats_bytes(int total_q, int num_seqs, int H) {
+    return (size_t)tile_slots(total_q, num_seqs, kStat) * H * 2 * kStat * sizeof(float);
+}
+
+bool make_maps(Maps *m, const LatentArgs &a, uint32_t box_q, uint32_t box_k) {
+    std::memset(m, 0, sizeof(*m));
+    const void *any = a.total_q ? a.q : a.k;
+    return make_map_heads(&m->q, a.q, a.Dk, a.H, a.total_q, box_q, any) && make_map_heads(&m->k, a.k, a.Dk, a.H, a.total_k, box_k, any) &&
+           make_map_heads(&m->v, a.v, a.Dv, a.H, a.total_k, box_k, any) &&
+           make_map_heads(&m->d_out, a.d_out, a.Dv, a.H, a.total_q, box_q, any) &&
+           (!a.Ds || (make_map_heads(&m->q_shared, a.q_shared, a.Ds, a.H, a.total_q, box_q, any) &&
+                      make_map_heads(&m->k_shared, a.k_shared, a.Ds, 1, a.total_k, box_k, any)));
+}
+
+}  // namespace
+
+size_t latent_backward_tc_scratch_bytes(int total_q, int total_k, int num_seqs, int H, int Ds) {
+    return stats_bytes(total_q, num_seqs, H) + (size_t)total_k * H * Ds * sizeof(float);
+}
+
+cudaError_t launch_latent_backward_tc(const LatentArgs &a0, void *scratch, cudaStream_t s) {
+    LatentArgs a = a0;
+    float *stats = static_cast<float *>(scratch);
+    a.dks_heads = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + stats_bytes(a.total_q, a.num_seqs, a.H));
+    cudaError_t e = allow_smem<latent_dkv_kernel>(232448);
+    if (e == cudaSuccess) e = allow_smem<latent_dq_kernel>(232448);
+    if (e != cudaSuccess) return e;
+    const int blocks = tile_slots(a.total_q, a.num_seqs, kStat), nk = (a.Dk + a.Ds) / 64, nv = a.Dv / 64;
+    if (a.total_q > 0) {
+        latent_stats_kernel<<<dim3(blocks, a.H), 256, 0, s>>>(a, stats);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    Maps m;
+    if (a.total_k > 0) {
+        if (!make_maps(&m, a, kRows, 128)) return cudaErrorInvalidValue;
+        latent_dkv_kernel<<<tile_slots(a.total_k, a.num_seqs, 128) * a.H, kThreads, smem_a(nk, nv), s>>>(m, a, stats, blocks);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (a.total_q > 0) {
+        if (!make_maps(&m, a, 128, kKeys)) return cudaErrorInvalidValue;
+        latent_dq_kernel<<<tile_slots(a.total_q, a.num_seqs, 128) * a.H, kThreads, smem_b(nk, nv), s>>>(m, a, stats, blocks);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return a.Ds ? launch_latent_shared_sum(a, s) : cudaSuccess;
+}
+
+}  // namespace rda

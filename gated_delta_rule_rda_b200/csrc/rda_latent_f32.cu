@@ -593,11 +593,7 @@ cudaError_t launch_latent_delta(const LatentArgs &a, cudaStream_t s) {
     const long rows = (long)a.total_q * a.H;
     const unsigned grid = (unsigned)((rows + 7) / 8);
     if (!grid) return cudaSuccess;
-    if (a.dtype == RDA_F32)
-        latent_delta_kernel<float><<<grid, 256, 0, s>>>((const float *)a.out, (const float *)a.d_out, a.delta, rows, a.Dv);
-    else
-        latent_delta_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>((const __nv_bfloat16 *)a.out,
-                                                               (const __nv_bfloat16 *)a.d_out, a.delta, rows, a.Dv);
+    latent_delta_kernel<float><<<grid, 256, 0, s>>>((const float *)a.out, (const float *)a.d_out, a.delta, rows, a.Dv);
     return cudaGetLastError();
 }
 
@@ -615,7 +611,7 @@ cudaError_t launch_latent_shared_sum(const LatentArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_latent_backward_f32(const LatentArgs &a, cudaStream_t s) {
-    return a.dtype == RDA_F32 ? backward_t<float>(a, s) : backward_t<__nv_bfloat16>(a, s);
+    return backward_t<float>(a, s);
 }
 
 cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s) {
