@@ -422,34 +422,48 @@ def rda_verify_drafts_workspace_bytes(B, T, V) -> int:
     return int(lib.rda_verify_drafts_workspace_bytes(B, T, V))
 
 
-def _need_like(t, name, shape, dtype, device):
-    """A contiguous CUDA tensor of this shape and type on this device."""
+def _need_like(t, name, shape, dtype, dev):
+    """A contiguous tensor of this shape and type on CUDA device number ``dev``."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
     if not t.is_cuda:
         raise ValueError("rda: tensors must be CUDA tensors (no CPU path exists)")
-    if t.device != device:
-        raise ValueError(f"rda: {name} is on {t.device}, other tensors on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"rda: {name} is on device {t.get_device()}, other tensors on {dev}")
     if t.dtype != dtype:
         raise TypeError(f"rda: {name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"rda: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"rda: {name} must be contiguous")
+    raise ValueError(f"rda: {name} must be contiguous")
 
 
-def _launch(fn, device, stream, *args):
-    """Calls a library function on ``device`` (its current stream unless one is
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(workspace, dev):
+    """(address, bytes) of a workspace tensor."""
+    if workspace.get_device() != dev:
+        raise ValueError("rda: the workspace is on another device than the tensors")
+    if not workspace.is_contiguous():
+        raise ValueError("rda: the workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _launch(fn, dev, stream, *args):
+    """Calls a library function on CUDA device number ``dev`` (its current stream unless one is
     given), whatever device is current."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"rda: the stream belongs to {stream.device}, the tensors to {device}")
-    s = ctypes.c_void_p(stream.cuda_stream)
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, s)
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"rda: the stream belongs to device {stream.device_index}, the tensors to {dev}")
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            code = fn(*args, s)
-    _check(code, fn.__name__)
+        with torch.cuda.device(dev):
+            code = fn(*args, stream.cuda_stream)
+    if code:
+        raise RdaError(code, fn.__name__)
 
 
 def _latent_sizes(q, k, v, q_shared, k_shared, cu_q, cu_k):
@@ -461,7 +475,7 @@ def _latent_sizes(q, k, v, q_shared, k_shared, cu_q, cu_k):
     total_q, H, Dk = q.shape
     total_k, Dv = k.shape[0], v.shape[2]
     Ds = 0 if k_shared is None else k_shared.shape[-1]
-    dev, dt = q.device, q.dtype
+    dev, dt = q.get_device(), q.dtype
     _dtype_code(q)
     _need_like(q, "q", (total_q, H, Dk), dt, dev)
     _need_like(k, "k", (total_k, H, Dk), dt, dev)
@@ -492,20 +506,20 @@ def rda_latent_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, scale, q_sha
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     total_q, total_k, H, Dk, Ds, Dv, N = sizes = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
-    dev = q.device
+    dev = q.get_device()
     if out is None:
-        out = torch.empty((total_q, H, Dv), dtype=q.dtype, device=dev)
+        out = q.new_empty((total_q, H, Dv))
     else:
         _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
     if lse is not None:
         _need_like(lse, "lse", (total_q, H), torch.float32, dev)
     elif return_lse:
-        lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((total_q, H), dtype=torch.float32)
     if workspace is None:
-        workspace = new_workspace(rda_latent_prefill_workspace_bytes(*sizes), dev)
-    _launch(lib.rda_latent_prefill, dev, stream, _ptr(q), _ptr(q_shared), _ptr(k), _ptr(k_shared), _ptr(v),
-            _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), N, total_q, total_k, _ptr(out), _ptr(lse), _dtype_code(q),
-            H, Dk, Ds, Dv, float(scale), int(bool(causal)), _ptr(workspace), workspace.numel())
+        workspace = new_workspace(rda_latent_prefill_workspace_bytes(*sizes), q.device)
+    _launch(lib.rda_latent_prefill, dev, stream, _addr(q), _addr(q_shared), _addr(k), _addr(k_shared), _addr(v),
+            _addr(cu_seqlens_q), _addr(cu_seqlens_k), N, total_q, total_k, _addr(out), _addr(lse), _dtype_code(q),
+            H, Dk, Ds, Dv, float(scale), int(bool(causal)), *_scratch(workspace, dev))
     return out, lse
 
 
@@ -518,7 +532,7 @@ def rda_latent_backward(q, k, v, out, lse, d_out, cu_seqlens_q, cu_seqlens_k=Non
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     total_q, total_k, H, Dk, Ds, Dv, N = sizes = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
-    dev = q.device
+    dev = q.get_device()
     _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
     _need_like(d_out, "d_out", (total_q, H, Dv), q.dtype, dev)
     _need_like(lse, "lse", (total_q, H), torch.float32, dev)
@@ -526,11 +540,11 @@ def rda_latent_backward(q, k, v, out, lse, d_out, cu_seqlens_q, cu_seqlens_k=Non
              dq_shared=torch.empty_like(q_shared) if Ds else None,
              dk_shared=torch.empty_like(k_shared) if Ds else None)
     if workspace is None:
-        workspace = new_workspace(rda_latent_backward_workspace_bytes(*sizes), dev)
-    _launch(lib.rda_latent_backward, dev, stream, _ptr(q), _ptr(q_shared), _ptr(k), _ptr(k_shared), _ptr(v),
-            _ptr(out), _ptr(lse), _ptr(d_out), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), N, total_q, total_k,
-            _ptr(g["dq"]), _ptr(g["dq_shared"]), _ptr(g["dk"]), _ptr(g["dk_shared"]), _ptr(g["dv"]),
-            _dtype_code(q), H, Dk, Ds, Dv, float(scale), int(bool(causal)), _ptr(workspace), workspace.numel())
+        workspace = new_workspace(rda_latent_backward_workspace_bytes(*sizes), q.device)
+    _launch(lib.rda_latent_backward, dev, stream, _addr(q), _addr(q_shared), _addr(k), _addr(k_shared), _addr(v),
+            _addr(out), _addr(lse), _addr(d_out), _addr(cu_seqlens_q), _addr(cu_seqlens_k), N, total_q, total_k,
+            _addr(g["dq"]), _addr(g["dq_shared"]), _addr(g["dk"]), _addr(g["dk_shared"]), _addr(g["dv"]),
+            _dtype_code(q), H, Dk, Ds, Dv, float(scale), int(bool(causal)), *_scratch(workspace, dev))
     return g
 
 
@@ -548,7 +562,7 @@ def rda_latent_decode(q, pages, block_table, seq_lens, *, scale, q_shared=None, 
     B, T, H, Dl = q.shape
     num_pages, page_size, D = pages.shape
     Ds = 0 if q_shared is None else q_shared.shape[-1]
-    dev, dt = q.device, q.dtype
+    dev, dt = q.get_device(), q.dtype
     code = _dtype_code(q)
     _need_like(q, "q", (B, T, H, Dl), dt, dev)
     if q_shared is not None:
@@ -557,18 +571,18 @@ def rda_latent_decode(q, pages, block_table, seq_lens, *, scale, q_shared=None, 
     _need_like(block_table, "block_table", (B, block_table.shape[1]), torch.int32, dev)
     _need_like(seq_lens, "seq_lens", (B,), torch.int32, dev)
     if out is None:
-        out = torch.empty((B, T, H, Dl), dtype=dt, device=dev)
+        out = q.new_empty((B, T, H, Dl))
     else:
         _need_like(out, "out", (B, T, H, Dl), dt, dev)
     if lse is not None:
         _need_like(lse, "lse", (B, T, H), torch.float32, dev)
     elif return_lse:
-        lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, T, H), dtype=torch.float32)
     if workspace is None:
-        workspace = new_workspace(rda_latent_decode_workspace_bytes(B, T, H, Dl, Ds), dev)
-    _launch(lib.rda_latent_decode, dev, stream, _ptr(q), _ptr(q_shared), _ptr(pages), _ptr(block_table),
-            _ptr(seq_lens), _ptr(out), _ptr(lse), code, B, T, H, Dl, Ds, num_pages, page_size,
-            block_table.shape[1], float(scale), _ptr(workspace), workspace.numel())
+        workspace = new_workspace(rda_latent_decode_workspace_bytes(B, T, H, Dl, Ds), q.device)
+    _launch(lib.rda_latent_decode, dev, stream, _addr(q), _addr(q_shared), _addr(pages), _addr(block_table),
+            _addr(seq_lens), _addr(out), _addr(lse), code, B, T, H, Dl, Ds, num_pages, page_size,
+            block_table.shape[1], float(scale), *_scratch(workspace, dev))
     return out, lse
 
 
@@ -584,7 +598,7 @@ def rda_verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, nu
         raise ValueError("rda: draft_tokens is [B, T], target_probs [B, T + 1, V]")
     B, T = draft_tokens.shape
     V = target_probs.shape[2]
-    dev = target_probs.device
+    dev = target_probs.get_device()
     _need_like(draft_tokens, "draft_tokens", (B, T), torch.int32, dev)
     _need_like(target_probs, "target_probs", (B, T + 1, V), torch.float32, dev)
     _need_like(uniforms, "uniforms", (B, T + 1), torch.float32, dev)
@@ -593,18 +607,17 @@ def rda_verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, nu
     if num_drafts is not None:
         _need_like(num_drafts, "num_drafts", (B,), torch.int32, dev)
     if tokens is None:
-        tokens = torch.empty((B, T + 1), dtype=torch.int32, device=dev)
+        tokens = draft_tokens.new_empty((B, T + 1))
     else:
         _need_like(tokens, "tokens", (B, T + 1), torch.int32, dev)
     if num_accepted is None:
-        num_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+        num_accepted = draft_tokens.new_empty((B,))
     else:
         _need_like(num_accepted, "num_accepted", (B,), torch.int32, dev)
     if workspace is None:
-        workspace = new_workspace(rda_verify_drafts_workspace_bytes(B, T, V), dev)
-    _launch(lib.rda_verify_drafts, dev, stream, _ptr(draft_tokens), _ptr(draft_probs), _ptr(target_probs),
-            _ptr(uniforms), _ptr(num_drafts), _ptr(tokens), _ptr(num_accepted), B, T, V, _ptr(workspace),
-            workspace.numel())
+        workspace = new_workspace(rda_verify_drafts_workspace_bytes(B, T, V), target_probs.device)
+    _launch(lib.rda_verify_drafts, dev, stream, _addr(draft_tokens), _addr(draft_probs), _addr(target_probs),
+            _addr(uniforms), _addr(num_drafts), _addr(tokens), _addr(num_accepted), B, T, V, *_scratch(workspace, dev))
     return tokens, num_accepted
 
 

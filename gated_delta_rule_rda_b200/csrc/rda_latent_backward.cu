@@ -11,7 +11,7 @@
 //
 //   keys    128 keys x 64 query rows a step:  S^T = K Q^T,  dP^T = V dO^T  (shared memory),
 //           then dV += P^T dO and dK += dS^T Q with P^T, dS^T as TMEM operands
-//   rows    128 query rows x 96 keys a step:  S = Q K^T,  dP = dO V^T,  then dQ += dS K
+//   rows    128 query rows x 80 keys a step:  S = Q K^T,  dP = dO V^T,  then dQ += dS K
 //
 // In both, one thread issues the MMAs: the next step's scores go out before this
 // step's P is consumed, so that the tensor pipe and the eight element-wise warps
@@ -43,9 +43,9 @@ constexpr int kRows = 64, kStagesA = 3;         // query rows of a step
 constexpr uint32_t kSmall = kRows * 128;        // 64 rows x 64 columns
 constexpr uint32_t kTdV = 0, kTdK = 128, kTS = 320, kTdP = 384, kTP = 448, kTdS = 480;
 // rows kernel
-constexpr int kKeys = 96, kStagesB = 2;         // keys of a step
-constexpr uint32_t kMid = kKeys * 128;          // 96 rows x 64 columns
-constexpr uint32_t kUdQ = 0, kUS = 192, kUdP = 288, kUdS = 384;
+constexpr int kKeys = 80, kStK = 3, kStV = 2;   // keys of a step; V is free again before K
+constexpr uint32_t kMid = kKeys * 128;          // 80 rows x 64 columns
+constexpr uint32_t kUdQ = 0, kUS = 192, kUdP = kUS + kKeys, kUdS = kUdP + kKeys;
 
 struct Maps {
     CUtensorMap q, q_shared, k, k_shared, v, d_out;
@@ -387,21 +387,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dQ: one CTA per (128 query rows, head).
 // ---------------------------------------------------------------------------
 struct BarsB {
-    uint64_t q_full, kv_full[kStagesB], kv_empty[kStagesB];
+    uint64_t q_full, k_full[kStK], k_empty[kStK], v_full[kStV], v_empty[kStV];
     uint64_t s_ready, s_free, dp_ready, dp_free, ds_ready, dq_done;
     uint32_t tmem;
     volatile int abort;
 };
-inline uint32_t smem_b(int nk, int nv) { return (nk + nv) * (kBig + kStagesB * kMid) + sizeof(BarsB) + 1024; }
+inline uint32_t smem_b(int nk, int nv) {
+    return (nk + nv) * kBig + (kStK * nk + kStV * nv) * kMid + sizeof(BarsB) + 1024;
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     latent_dq_kernel(const __grid_constant__ Maps maps, const LatentArgs a, const float *stats, int stat_blocks) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = align_1024(smem_raw);
     const int nd = a.Dk / 64, nk = (a.Dk + a.Ds) / 64, nv = a.Dv / 64;
-    const uint32_t stage = (nk + nv) * kMid;
-    uint8_t *q_s = sm, *o_s = q_s + nk * kBig, *st_s = o_s + nv * kBig;       // a stage: K, V
-    BarsB &B = *reinterpret_cast<BarsB *>(st_s + kStagesB * stage);
+    uint8_t *q_s = sm, *o_s = q_s + nk * kBig, *k_s = o_s + nv * kBig, *v_s = k_s + kStK * nk * kMid;
+    BarsB &B = *reinterpret_cast<BarsB *>(v_s + kStV * nv * kMid);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Waiter w{&B.abort, a.err, a.wait_ns};
 
@@ -421,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 32) {
         mbar_init(&B.q_full, 1);
-        for (int i = 0; i < kStagesB; ++i) mbar_init(&B.kv_full[i], 1), mbar_init(&B.kv_empty[i], 1);
+        for (int i = 0; i < kStK; ++i) mbar_init(&B.k_full[i], 1), mbar_init(&B.k_empty[i], 1);
+        for (int i = 0; i < kStV; ++i) mbar_init(&B.v_full[i], 1), mbar_init(&B.v_empty[i], 1);
         mbar_init(&B.s_ready, 1);
         mbar_init(&B.dp_ready, 1);
         mbar_init(&B.dq_done, 1);
@@ -447,25 +449,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(q_s + c * kBig, c < nd ? &maps.q : &maps.q_shared, &B.q_full, (c < nd ? c : c - nd) * 64, h,
                             sq.start + r0);
             for (int c = 0; c < nv; ++c) tma_load_3d(o_s + c * kBig, &maps.d_out, &B.q_full, c * 64, h, sq.start + r0);
-            RingPos p;
-            int loaded = 0;
-            for (; loaded < steps; ++loaded) {
-                if (loaded >= kStagesB && !w.wait(&B.kv_empty[p.slot], p.phase ^ 1)) break;
-                const int row = sk.start + loaded * kKeys;
-                uint8_t *dst = st_s + p.slot * stage;
-                mbar_arrive_expect_tx(&B.kv_full[p.slot], stage);
+            RingPos pk, pv;
+            int loaded_k = 0, loaded_v = 0;
+            for (int i = 0; i < steps; ++i) {
+                const int row = sk.start + i * kKeys;
+                if (i >= kStK && !w.wait(&B.k_empty[pk.slot], pk.phase ^ 1)) break;
+                mbar_arrive_expect_tx(&B.k_full[pk.slot], nk * kMid);
                 for (int c = 0; c < nk; ++c)
-                    tma_load_3d(dst + c * kMid, c < nd ? &maps.k : &maps.k_shared, &B.kv_full[p.slot],
+                    tma_load_3d(k_s + (pk.slot * nk + c) * kMid, c < nd ? &maps.k : &maps.k_shared, &B.k_full[pk.slot],
                                 (c < nd ? c : c - nd) * 64, c < nd ? h : 0, row);
+                pk.next(kStK);
+                ++loaded_k;
+                if (i >= kStV && !w.wait(&B.v_empty[pv.slot], pv.phase ^ 1)) break;
+                mbar_arrive_expect_tx(&B.v_full[pv.slot], nv * kMid);
                 for (int c = 0; c < nv; ++c)
-                    tma_load_3d(dst + (nk + c) * kMid, &maps.v, &B.kv_full[p.slot], c * 64, h, row);
-                p.next(kStagesB);
+                    tma_load_3d(v_s + (pv.slot * nv + c) * kMid, &maps.v, &B.v_full[pv.slot], c * 64, h, row);
+                pv.next(kStV);
+                ++loaded_v;
             }
             if (B.abort) {
                 const uint64_t t0 = Waiter::now();
                 w.drain(&B.q_full, 0, t0);
-                for (int i = max(0, loaded - kStagesB); i < loaded; ++i)
-                    w.drain(&B.kv_full[i % kStagesB], (i / kStagesB) & 1, t0);
+                for (int i = max(0, loaded_k - kStK); i < loaded_k; ++i) w.drain(&B.k_full[i % kStK], (i / kStK) & 1, t0);
+                for (int i = max(0, loaded_v - kStV); i < loaded_v; ++i) w.drain(&B.v_full[i % kStV], (i / kStV) & 1, t0);
             }
         }
         __syncwarp();
@@ -474,7 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one() && steps > 0) {
             const uint32_t idN = idesc_bf16(128, kKeys, 0, 0), idQ = idesc_bf16(128, 64 * nk, 0, 1);
             const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024, kSw128), dO = smem_desc(smem_u32(o_s), 16, 1024, kSw128);
-            const uint64_t ds = smem_desc(smem_u32(st_s), 16, 1024, kSw128), dm = smem_desc(smem_u32(st_s), kMid, 1024, kSw128);
+            const uint64_t dk = smem_desc(smem_u32(k_s), 16, 1024, kSw128), dv = smem_desc(smem_u32(v_s), 16, 1024, kSw128);
+            const uint64_t dm = smem_desc(smem_u32(k_s), kMid, 1024, kSw128);        // K, MN-major
             bool ok = w.wait(&B.q_full, 0);
             auto product = [&](uint32_t d, uint64_t da, uint64_t db, int chunks) {
                 for (int c = 0; c < chunks; ++c)
@@ -482,20 +489,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; ++k)
                         mma_bf16(d, da + c * (kBig / 16) + 2 * k, db + c * (kMid / 16) + 2 * k, idN, c > 0 || k > 0);
             };
-            RingPos next, now;
+            RingPos next, now, vs;
             for (int i = -1; i < steps; ++i) {
                 if (i + 1 < steps) {
-                    const uint64_t off = next.slot * (stage / 16);
-                    ok = w.wait(&B.kv_full[next.slot], next.phase) && ok;
+                    ok = w.wait(&B.k_full[next.slot], next.phase) && ok;
                     if (i >= 0) ok = w.wait(&B.s_free, i & 1) && ok;
                     tc_fence_after();
-                    if (ok) product(tmem + kUS, dq, ds + off, nk);
+                    if (ok) product(tmem + kUS, dq, dk + next.slot * nk * (kMid / 16), nk);
                     mma_commit(&B.s_ready);
+                    next.next(kStK);
+                    ok = w.wait(&B.v_full[vs.slot], vs.phase) && ok;
                     if (i >= 0) ok = w.wait(&B.dp_free, i & 1) && ok;
                     tc_fence_after();
-                    if (ok) product(tmem + kUdP, dO, ds + off + nk * (kMid / 16), nv);
+                    if (ok) product(tmem + kUdP, dO, dv + vs.slot * nv * (kMid / 16), nv);
                     mma_commit(&B.dp_ready);
-                    next.next(kStagesB);
+                    mma_commit(&B.v_empty[vs.slot]);
+                    vs.next(kStV);
                 }
                 if (i < 0) continue;
                 ok = w.wait(&B.ds_ready, i & 1) && ok;
@@ -503,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok) {
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        mma_bf16_ta(tmem + kUdQ, tmem + kUdS + 8 * k, dm + now.slot * (stage / 16) + 128 * k, idQ, i > 0 || k > 0);
+                        mma_bf16_ta(tmem + kUdQ, tmem + kUdS + 8 * k, dm + now.slot * nk * (kMid / 16) + 128 * k, idQ, i > 0 || k > 0);
                 }
-                mma_commit(&B.kv_empty[now.slot]);
+                mma_commit(&B.k_empty[now.slot]);
                 mma_commit(&B.dq_done);
-                now.next(kStagesB);
+                now.next(kStK);
             }
             if (B.abort) w.drain(&B.dq_done, (steps - 1) & 1, Waiter::now());
         }
@@ -515,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------------------ element-wise: my query row, half of the keys
         constexpr int C = kKeys / 2;
+        static_assert(C == 40, "loads of 32 + 8 columns");
         const int quad = warp & 3, half = warp >= 6, r = 32 * quad + lane, row = r0 + r;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
         const uint32_t t_s = tmem + kUS + C * half + lanes, t_dp = tmem + kUdP + C * half + lanes,
@@ -536,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.wait(&B.s_ready, i & 1);
             tc_fence_after();
             tmem_ld32(t_s, x);
-            tmem_ld16(t_s + 32, x + 32);
+            tmem_ld8(t_s + 32, x + 32);
             tmem_wait_ld();
             tc_fence_before();
             mbar_arrive(&B.s_free);
@@ -545,15 +555,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int keys = sk.len - i * kKeys;
             if (keys < kKeys) {
                 // keys behind the sequence may hold anything: 0 x NaN must not reach the sums
-                w.wait(&B.kv_full[p.slot], p.phase);
-                zero_rows(st_s + p.slot * stage, kMid, nk, keys, kKeys);
+                w.wait(&B.k_full[p.slot], p.phase);
+                zero_rows(k_s + p.slot * nk * kMid, kMid, nk, keys, kKeys);
                 fence_proxy_async_smem();
             }
             w.wait(&B.dp_ready, i & 1);
             tc_fence_after();
             float y[C];
             tmem_ld32(t_dp, y);
-            tmem_ld16(t_dp + 32, y + 32);
+            tmem_ld8(t_dp + 32, y + 32);
             tmem_wait_ld();
             tc_fence_before();
             mbar_arrive(&B.dp_free);
@@ -568,11 +578,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i > 0) w.wait(&B.dq_done, (i - 1) & 1);
             tc_fence_after();
             tmem_st16(t_ds, pk);
-            tmem_st8(t_ds + 16, pk + 16);
+            tmem_st4(t_ds + 16, pk + 16);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&B.ds_ready);
-            p.next(kStagesB);
+            p.next(kStK);
         }
         if (steps > 0) {
             w.wait(&B.dq_done, (steps - 1) & 1);

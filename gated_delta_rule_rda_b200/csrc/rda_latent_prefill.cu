@@ -53,7 +53,7 @@ struct Maps {
 };
 
 struct Bars {
-    uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t q_full[kQ], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_ready[kQ], s_free[kQ], p_ready[kQ], pv_done[kQ];
     uint32_t tmem;
     volatile int abort;
@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
         tmem_relinquish();
     }
     if (tid == 32) {
-        mbar_init(&B.q_full, 1);
+        mbar_init(&B.q_full[0], 1);
+        mbar_init(&B.q_full[1], 1);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&B.k_full[i], 1);
             mbar_init(&B.k_empty[i], 1);
@@ -120,12 +121,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (elect_one() && nt > 0) {
-            const int tiles = n1 > 0 ? 2 : 1;
-            mbar_arrive_expect_tx(&B.q_full, tiles * nk * kQChunk);
-            for (int q = 0; q < tiles; ++q)
+            // in the order of use: the first tile's queries, K, the second tile's queries, V
+            auto queries = [&](int q) {
+                mbar_arrive_expect_tx(&B.q_full[q], nk * kQChunk);
                 for (int c = 0; c < nk; ++c)
-                    tma_load_3d(q_s + (q * nk + c) * kQChunk, c < nd ? &maps.q : &maps.q_shared, &B.q_full,
+                    tma_load_3d(q_s + (q * nk + c) * kQChunk, c < nd ? &maps.q : &maps.q_shared, &B.q_full[q],
                                 (c < nd ? c : c - nd) * 64, h, sq.start + r0 + q * kBM);
+            };
+            if (n0 > 0) queries(0);
             RingPos p;
             bool go = true;
             int loaded_k = 0, loaded_v = 0;
@@ -138,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
                     tma_load_3d(k_s + (p.slot * nk + c) * kKChunk, c < nd ? &maps.k : &maps.k_shared, &B.k_full[p.slot],
                                 (c < nd ? c : c - nd) * 64, c < nd ? h : 0, row);
                 ++loaded_k;
+                if (j == 0 && n1 > 0) queries(1);
                 if (j >= kStages) go = go && w.wait(&B.v_empty[p.slot], p.phase ^ 1);
                 if (!go) break;
                 mbar_arrive_expect_tx(&B.v_full[p.slot], nv * kKChunk);
@@ -149,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
             if (B.abort) {
                 // copies in flight land before the CTA leaves: the last ones of each stage
                 const uint64_t t0 = Waiter::now();
-                w.drain(&B.q_full, 0, t0);
+                if (n0 > 0) w.drain(&B.q_full[0], 0, t0);
+                if (n1 > 0) w.drain(&B.q_full[1], 0, t0);
                 for (int i = max(0, loaded_k - kStages); i < loaded_k; ++i)
                     w.drain(&B.k_full[i % kStages], (i / kStages) & 1, t0);
                 for (int i = max(0, loaded_v - kStages); i < loaded_v; ++i)
@@ -163,9 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
             const uint32_t idS = idesc_bf16(kBM, kBN, 0, 0), idO = idesc_bf16(kBM, a.Dv, 0, 1);
             const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024, kSw128), dk = smem_desc(smem_u32(k_s), 16, 1024, kSw128);
             const uint64_t dv = smem_desc(smem_u32(v_s), kKChunk, 1024, kSw128);
-            bool ok = w.wait(&B.q_full, 0);
+            bool ok = true;
             auto scores = [&](int q, int j) {
-                if (j > 0) ok = w.wait(&B.s_free[q], (j - 1) & 1) && ok;
+                ok = (j > 0 ? w.wait(&B.s_free[q], (j - 1) & 1) : w.wait(&B.q_full[q], 0)) && ok;
                 tc_fence_after();
                 if (ok)
                     for (int c = 0; c < nk; ++c) {
@@ -254,23 +259,24 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
                 m = top;
             }
             const float base = m == -INFINITY ? 0.f : m * sc;
+            // probabilities, and their sums in four chains (a branch inside would keep the exponentials in lockstep)
             float p0 = 0.f, p1 = 0.f, p2 = 0.f, p3 = 0.f;
             uint32_t pk[kBN / 2];
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < kBN; ++i) s[i] = i < left ? ex2(fmaf(s[i], sc, -base)) : 0.f;     // also for a scale of 0
+            } else {
+#pragma unroll
+                for (int i = 0; i < kBN; ++i) s[i] = ex2(fmaf(s[i], sc, -base));
+            }
 #pragma unroll
             for (int i = 0; i < kBN; i += 4) {
-                float x[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) x[u] = ex2(fmaf(s[i + u], sc, -base));
-                if (masked) {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) x[u] = i + u < left ? x[u] : 0.f;       // also for a scale of 0
-                }
-                p0 += x[0];
-                p1 += x[1];
-                p2 += x[2];
-                p3 += x[3];
-                pk[i / 2] = pack2(x[0], x[1]);
-                pk[i / 2 + 1] = pack2(x[2], x[3]);
+                p0 += s[i];
+                p1 += s[i + 1];
+                p2 += s[i + 2];
+                p3 += s[i + 3];
+                pk[i / 2] = pack2(s[i], s[i + 1]);
+                pk[i / 2 + 1] = pack2(s[i + 2], s[i + 3]);
             }
             l = fmaf(l, f, (p0 + p1) + (p2 + p3));
             if (j > 0) w.wait(&B.pv_done[q], (j - 1) & 1);           // P and O are free
