@@ -385,10 +385,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // dQ: one CTA per (128 query rows, head).
+//
+// delta from the stored result carries that result's rounding to bf16, an error
+// of up to 2^-8 sum |do o| that all ds of a row share.  Over many keys the result
+// is an average and small; over few it is as large as v, and with one visible key
+// ds should vanish.  Tiles that see at most two steps of keys therefore run a
+// pass ahead: sum_j p_ij (dp_ij - delta_i) is what delta lacks, and delta is
+// corrected before it is used, here and (through the statistics) for dK.
 // ---------------------------------------------------------------------------
+constexpr int kExactSteps = 2;
 struct BarsB {
     uint64_t q_full, k_full[kStK], k_empty[kStK], v_full[kStV], v_empty[kStV];
     uint64_t s_ready, s_free, dp_ready, dp_free, ds_ready, dq_done;
+    float lack[2][128];                          // sum of ds of a row, by half of the columns
     uint32_t tmem;
     volatile int abort;
 };
@@ -397,7 +406,7 @@ inline uint32_t smem_b(int nk, int nv) {
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_dq_kernel(const __grid_constant__ Maps maps, const LatentArgs a, const float *stats, int stat_blocks) {
+    latent_dq_kernel(const __grid_constant__ Maps maps, const LatentArgs a, float *stats, int stat_blocks) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = align_1024(smem_raw);
     const int nd = a.Dk / 64, nk = (a.Dk + a.Ds) / 64, nv = a.Dv / 64;
@@ -414,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows = min(128, sq.len - r0);
     if (rows <= 0) return;
     const int end = a.causal ? min(sk.len, r0 + rows + more) : sk.len;
-    const int steps = end > 0 ? (end + kKeys - 1) / kKeys : 0;
+    const int tiles = end > 0 ? (end + kKeys - 1) / kKeys : 0;
+    const int ahead = tiles <= kExactSteps ? tiles : 0, steps = ahead + tiles;      // steps before the first that counts
 
     if (warp == 0) {
         tmem_alloc(&B.tmem, kCols);
@@ -452,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             RingPos pk, pv;
             int loaded_k = 0, loaded_v = 0;
             for (int i = 0; i < steps; ++i) {
-                const int row = sk.start + i * kKeys;
+                const int row = sk.start + (i < ahead ? i : i - ahead) * kKeys;
                 if (i >= kStK && !w.wait(&B.k_empty[pk.slot], pk.phase ^ 1)) break;
                 mbar_arrive_expect_tx(&B.k_full[pk.slot], nk * kMid);
                 for (int c = 0; c < nk; ++c)
@@ -509,10 +519,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i < 0) continue;
                 ok = w.wait(&B.ds_ready, i & 1) && ok;
                 tc_fence_after();
-                if (ok) {
+                if (ok && i >= ahead) {
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        mma_bf16_ta(tmem + kUdQ, tmem + kUdS + 8 * k, dm + now.slot * nk * (kMid / 16) + 128 * k, idQ, i > 0 || k > 0);
+                        mma_bf16_ta(tmem + kUdQ, tmem + kUdS + 8 * k, dm + now.slot * nk * (kMid / 16) + 128 * k, idQ, i > ahead || k > 0);
                 }
                 mma_commit(&B.k_empty[now.slot]);
                 mma_commit(&B.dq_done);
@@ -531,9 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                        t_ds = tmem + kUdS + C / 2 * half + lanes;
         const float sc = a.scale * kLog2e;
         const int limit = r >= rows ? 0 : a.causal ? min(sk.len, row + more + 1) : sk.len;      // keys that my row sees
-        float lse = INFINITY, delta = 0.f;
+        float lse = INFINITY, delta = 0.f, lack = 0.f;
+        float *st = stats + ((size_t)h * stat_blocks + stat_block(a, n, row)) * 2 * kStat + row % kStat;
         if (r < rows) {
-            const float *st = stats + ((size_t)h * stat_blocks + stat_block(a, n, row)) * 2 * kStat + row % kStat;
             lse = st[0];
             delta = st[kStat];
         }
@@ -541,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < steps; ++i) {
             float x[C];
             uint32_t pk[C / 2];
-            const int left = limit - i * kKeys - C * half;
+            const int k0 = (i < ahead ? i : i - ahead) * kKeys, left = limit - k0 - C * half;
             const bool masked = __any_sync(0xffffffffu, left < C);
             w.wait(&B.s_ready, i & 1);
             tc_fence_after();
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&B.s_free);
 #pragma unroll
             for (int c = 0; c < C; ++c) x[c] = ex2(fmaf(x[c], sc, -lse));
-            const int keys = sk.len - i * kKeys;
+            const int keys = sk.len - k0;
             if (keys < kKeys) {
                 // keys behind the sequence may hold anything: 0 x NaN must not reach the sums
                 w.wait(&B.k_full[p.slot], p.phase);
@@ -572,6 +582,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (masked) {
 #pragma unroll
                 for (int c = 0; c < C; ++c) x[c] = c < left ? x[c] : 0.f;
+            }
+            if (i < ahead) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) lack += x[c];
+                if (i == ahead - 1) {
+                    B.lack[half][r] = lack;
+                    named_bar_sync(1, 256);
+                    delta += B.lack[0][r] + B.lack[1][r];
+                    if (half == 0 && r < rows) st[kStat] = delta;
+                }
+                mbar_arrive(&B.ds_ready);
+                p.next(kStK);
+                continue;
             }
 #pragma unroll
             for (int c = 0; c < C; c += 2) pk[c / 2] = pack2(x[c], x[c + 1]);
@@ -638,14 +661,15 @@ cudaError_t launch_latent_backward_tc(const LatentArgs &a0, void *scratch, cudaS
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     Maps m;
-    if (a.total_k > 0) {
-        if (!make_maps(&m, a, kRows, 128)) return cudaErrorInvalidValue;
-        latent_dkv_kernel<<<tile_slots(a.total_k, a.num_seqs, 128) * a.H, kThreads, smem_a(nk, nv), s>>>(m, a, stats, blocks);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
+    // dQ first: it corrects the statistics that dK uses
     if (a.total_q > 0) {
         if (!make_maps(&m, a, 128, kKeys)) return cudaErrorInvalidValue;
         latent_dq_kernel<<<tile_slots(a.total_q, a.num_seqs, 128) * a.H, kThreads, smem_b(nk, nv), s>>>(m, a, stats, blocks);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (a.total_k > 0) {
+        if (!make_maps(&m, a, kRows, 128)) return cudaErrorInvalidValue;
+        latent_dkv_kernel<<<tile_slots(a.total_k, a.num_seqs, 128) * a.H, kThreads, smem_a(nk, nv), s>>>(m, a, stats, blocks);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     return a.Ds ? launch_latent_shared_sum(a, s) : cudaSuccess;

@@ -26,58 +26,61 @@ constexpr int kLdP = kTile + 4;
 // Rows [row0, row0 + n) of head h as fp32 into dst[64][ld]: `part` ([rows, H, D0])
 // and behind it `shared` ([rows, Hs, D1], the same for every head if Hs = 1).
 // Rows from n on are zero, whatever lies behind a sequence.
-template <typename T>
+template <typename T, int ROWS = kTile, int NT = kThreads>
 __device__ __forceinline__ void load_rows(float *dst, int ld, const T *part, int D0, const T *shared, int D1, int Hs,
                                           long row0, int n, int H, int h) {
-    const int per = (D0 + D1) / 4;
-    for (int e = threadIdx.x; e < kTile * per; e += kThreads) {
-        const int r = e / per, c = (e % per) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n) {
-            const size_t row = (size_t)(row0 + r);
-            x = c < D0 ? Io<T>::ld4(part + (row * H + h) * D0 + c)
-                       : Io<T>::ld4(shared + (row * Hs + (Hs == 1 ? 0 : h)) * D1 + (c - D0));
+    // 16 threads a row
+    const int r0 = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * 4;
+#pragma unroll
+    for (int r = r0; r < ROWS; r += NT / 16) {
+        const size_t row = (size_t)(row0 + r);
+#pragma unroll 3
+        for (int c = c0; c < D0 + D1; c += 64) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < n)
+                x = c < D0 ? Io<T>::ld4(part + (row * H + h) * D0 + c)
+                           : Io<T>::ld4(shared + (row * Hs + (Hs == 1 ? 0 : h)) * D1 + (c - D0));
+            *reinterpret_cast<float4 *>(dst + r * ld + c) = x;
         }
-        *reinterpret_cast<float4 *>(dst + r * ld + c) = x;
     }
 }
 
-// acc[i][j] += a[4 ty + i] . b[tx + 16 j] over D
-__device__ __forceinline__ void dot44(float (&acc)[4][4], const float *a, int lda, const float *b, int ldb, int D) {
+// acc[i][j] += a[RI ty + i] . b[tx + 16 j] over D
+template <int RI>
+__device__ __forceinline__ void dot(float (&acc)[RI][4], const float *a, int lda, const float *b, int ldb, int D) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const float *ar = a + 4 * ty * lda, *br = b + tx * ldb;
+    const float *ar = a + RI * ty * lda, *br = b + tx * ldb;
 #pragma unroll 2
     for (int d = 0; d < D; d += 4) {
-        float4 x[4], y[4];
+        float4 x[RI], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = *reinterpret_cast<const float4 *>(ar + i * lda + d);
-            y[i] = *reinterpret_cast<const float4 *>(br + 16 * i * ldb + d);
-        }
+        for (int i = 0; i < RI; ++i) x[i] = *reinterpret_cast<const float4 *>(ar + i * lda + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const float4 *>(br + 16 * i * ldb + d);
+#pragma unroll
+        for (int i = 0; i < RI; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
     }
 }
 
-// acc[i][4 c ..] += sum_j w[4 ty + i][j] b[j][64 c + 4 tx ..]   (w row-major)
-template <int NC>
-__device__ __forceinline__ void rows_times(float (&acc)[4][NC][4], const float *w, const float *b, int ldb) {
+// acc[i][4 c ..] += sum_j w[RI ty + i][j] b[j][64 c + 4 tx ..]   (w row-major)
+template <int RI, int NC>
+__device__ __forceinline__ void rows_times(float (&acc)[RI][NC][4], const float *w, const float *b, int ldb) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll 1
     for (int j = 0; j < kTile; j += 4) {
-        float4 x[4];
+        float4 x[RI];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(w + (4 * ty + i) * kLdP + j);
+        for (int i = 0; i < RI; ++i) x[i] = *reinterpret_cast<const float4 *>(w + (RI * ty + i) * kLdP + j);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const float4 y = *reinterpret_cast<const float4 *>(b + (j + u) * ldb + 64 * c + 4 * tx);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < RI; ++i) {
                     const float p = u == 0 ? x[i].x : u == 1 ? x[i].y : u == 2 ? x[i].z : x[i].w;
                     acc[i][c][0] = fmaf(p, y.x, acc[i][c][0]);
                     acc[i][c][1] = fmaf(p, y.y, acc[i][c][1]);
@@ -111,14 +114,14 @@ __device__ __forceinline__ void cols_times(float (&acc)[4][NC][4], const float *
 
 // Columns [64 c, 64 c + 64) of 64 rows to out ([rows, H, D0]) or, from column
 // D0 on, to shared ([rows, H, D1]).
-template <typename T, typename U, int NC>
-__device__ __forceinline__ void store_rows(const float (&acc)[4][NC][4], float f, T *out, int D0, U *shared, int D1,
+template <typename T, typename U, int RI, int NC>
+__device__ __forceinline__ void store_rows(const float (&acc)[RI][NC][4], float f, T *out, int D0, U *shared, int D1,
                                            long row0, int n, int H, int h) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (4 * ty + i >= n) continue;
-        const size_t row = (size_t)(row0 + 4 * ty + i) * H + h;
+    for (int i = 0; i < RI; ++i) {
+        if (RI * ty + i >= n) continue;
+        const size_t row = (size_t)(row0 + RI * ty + i) * H + h;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int col = 64 * c + 4 * tx;
@@ -134,38 +137,42 @@ __device__ __forceinline__ bool seen(const LatentArgs &a, int i, int j, int lq, 
 }
 
 // ---------------------------------------------------------------------------
-// Forward: one CTA per (64 query rows, head), online softmax over key tiles.
+// Forward: one CTA per (RI NT / 16 query rows, head), online softmax over key
+// tiles.  RI = 4 with 512 threads (128 rows) reads each operand for four products
+// and keeps 16 warps on an SM; RI = 1 with 256 threads (16 rows) makes eight times
+// as many CTAs, for calls that would leave SMs empty.
 // ---------------------------------------------------------------------------
-template <typename T, int NDV>
-__global__ void __launch_bounds__(kThreads) latent_forward_f32_kernel(LatentArgs a) {
+template <typename T, int NDV, int RI, int NT>
+__global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a) {
     extern __shared__ __align__(16) float smem[];
+    constexpr int M = RI * NT / 16;
     const int D = a.Dk + a.Ds, ld = D + 4, ldv = 64 * NDV + 4;
-    float *Qs = smem, *Ks = Qs + kTile * ld, *Vs = Ks + kTile * ld, *Ps = Vs + kTile * ldv;
+    float *Qs = smem, *Ks = Qs + M * ld, *Vs = Ks + kTile * ld, *Ps = Vs + kTile * ldv;
     int t;
     // the last tiles of a sequence see the most keys: start with them
-    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, kTile, (int)(gridDim.x - 1 - blockIdx.x), &t);
+    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, M, (int)(gridDim.x - 1 - blockIdx.x), &t);
     const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
-    const int h = blockIdx.y, r0 = t * kTile;
-    const int rows = min(kTile, sq.len - r0);
+    const int h = blockIdx.y, r0 = t * M;
+    const int rows = min(M, sq.len - r0);
     if (rows <= 0) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_rows<T>(Qs, ld, (const T *)a.q, a.Dk, (const T *)a.q_shared, a.Ds, a.H, sq.start + r0, rows, a.H, h);
-    float o[4][NDV][4] = {}, m[4], l[4];
+    load_rows<T, M, NT>(Qs, ld, (const T *)a.q, a.Dk, (const T *)a.q_shared, a.Ds, a.H, sq.start + r0, rows, a.H, h);
+    float o[RI][NDV][4] = {}, m[RI], l[RI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    for (int i = 0; i < RI; ++i) m[i] = -INFINITY, l[i] = 0.f;
     const int kend = a.causal ? min(sk.len, r0 + rows + sk.len - sq.len) : sk.len;
     for (int k0 = 0; k0 < kend; k0 += kTile) {
         __syncthreads();
-        load_rows<T>(Ks, ld, (const T *)a.k, a.Dk, (const T *)a.k_shared, a.Ds, 1, sk.start + k0,
+        load_rows<T, kTile, NT>(Ks, ld, (const T *)a.k, a.Dk, (const T *)a.k_shared, a.Ds, 1, sk.start + k0,
                      min(kTile, sk.len - k0), a.H, h);
-        load_rows<T>(Vs, ldv, (const T *)a.v, 64 * NDV, (const T *)nullptr, 0, 1, sk.start + k0,
+        load_rows<T, kTile, NT>(Vs, ldv, (const T *)a.v, 64 * NDV, (const T *)nullptr, 0, 1, sk.start + k0,
                      min(kTile, sk.len - k0), a.H, h);
         __syncthreads();
-        float s[4][4] = {};
-        dot44(s, Qs, ld, Ks, ld, D);
+        float s[RI][4] = {};
+        dot<RI>(s, Qs, ld, Ks, ld, D);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + 4 * ty + i;
+        for (int i = 0; i < RI; ++i) {
+            const int r = r0 + RI * ty + i;
             float top = m[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -186,18 +193,18 @@ __global__ void __launch_bounds__(kThreads) latent_forward_f32_kernel(LatentArgs
             for (int j = 0; j < 4; ++j) {
                 const float p = expf(s[i][j] - base);
                 l[i] += p;
-                Ps[(4 * ty + i) * kLdP + tx + 16 * j] = p;
+                Ps[(RI * ty + i) * kLdP + tx + 16 * j] = p;
             }
         }
         __syncthreads();
-        rows_times<NDV>(o, Ps, Vs, ldv);
+        rows_times<RI, NDV>(o, Ps, Vs, ldv);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RI; ++i) {
 #pragma unroll
         for (int off = 8; off; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
-        const int r = r0 + 4 * ty + i;
-        if (a.lse && tx == 0 && 4 * ty + i < rows)
+        const int r = r0 + RI * ty + i;
+        if (a.lse && tx == 0 && RI * ty + i < rows)
             a.lse[(size_t)(sq.start + r) * a.H + h] = l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
         const float f = l[i] > 0.f ? 1.f / l[i] : 0.f;
 #pragma unroll
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) latent_forward_f32_kernel(LatentArgs
 #pragma unroll
             for (int u = 0; u < 4; ++u) o[i][c][u] *= f;
     }
-    store_rows<T, T, NDV>(o, 1.f, (T *)a.out, 64 * NDV, (T *)nullptr, 0, sq.start + r0, rows, a.H, h);
+    store_rows<T, T, RI, NDV>(o, 1.f, (T *)a.out, 64 * NDV, (T *)nullptr, 0, sq.start + r0, rows, a.H, h);
 }
 
 // ---------------------------------------------------------------------------
@@ -221,8 +228,8 @@ __device__ __forceinline__ void tile_grads(const LatentArgs &a, const float *Qs,
                                            const float *delta_s, int r0, int k0, int lq, int lk, float *Ps, float *Ss) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float s[4][4] = {}, dp[4][4] = {};
-    dot44(s, Qs, ld, Ks, ld, D);
-    dot44(dp, Os, ldv, Vs, ldv, Dv);
+    dot<4>(s, Qs, ld, Ks, ld, D);
+    dot<4>(dp, Os, ldv, Vs, ldv, Dv);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
@@ -274,8 +281,8 @@ __global__ void __launch_bounds__(kThreads) latent_dkv_f32_kernel(LatentArgs a) 
         cols_times<NDV>(dv, Ps, Os, ldv);
         cols_times<ND>(dk, Ss, Qs, ld);
     }
-    store_rows<T, T, NDV>(dv, 1.f, (T *)a.dv, Dv, (T *)nullptr, 0, sk.start + k0, keys, a.H, h);
-    store_rows<T, float, ND>(dk, a.scale, (T *)a.dk, a.Dk, a.dks_heads, a.Ds, sk.start + k0, keys, a.H, h);
+    store_rows<T, T, 4, NDV>(dv, 1.f, (T *)a.dv, Dv, (T *)nullptr, 0, sk.start + k0, keys, a.H, h);
+    store_rows<T, float, 4, ND>(dk, a.scale, (T *)a.dk, a.Dk, a.dks_heads, a.Ds, sk.start + k0, keys, a.H, h);
 }
 
 template <typename T, int ND, int NDV>
@@ -303,9 +310,9 @@ __global__ void __launch_bounds__(kThreads) latent_dq_f32_kernel(LatentArgs a) {
         __syncthreads();
         tile_grads(a, Qs, Ks, ld, D, Os, Vs, ldv, Dv, lse_s, delta_s, r0, k0, sq.len, sk.len, nullptr, Ss);
         __syncthreads();
-        rows_times<ND>(dq, Ss, Ks, ld);
+        rows_times<4, ND>(dq, Ss, Ks, ld);
     }
-    store_rows<T, T, ND>(dq, a.scale, (T *)a.dq, a.Dk, (T *)a.dq_shared, a.Ds, sq.start + r0, rows, a.H, h);
+    store_rows<T, T, 4, ND>(dq, a.scale, (T *)a.dq, a.Dk, (T *)a.dq_shared, a.Ds, sq.start + r0, rows, a.H, h);
 }
 
 // delta_i = d_out_i . out_i: one warp per (row, head).
@@ -341,14 +348,21 @@ __global__ void __launch_bounds__(256) latent_shared_sum_kernel(const float *par
     Io<T>::st4(out + row * Ds + c, x);
 }
 
-template <typename T, int NDV> cudaError_t forward_nv(const LatentArgs &a, cudaStream_t s) {
-    constexpr size_t most = sizeof(float) * kTile * (2 * (192 + 4) + (64 * NDV + 4) + kLdP);
-    const cudaError_t e = allow_smem<latent_forward_f32_kernel<T, NDV>>(most);
+template <typename T, int NDV, int RI, int NT> cudaError_t forward_ri(const LatentArgs &a, cudaStream_t s) {
+    constexpr int M = RI * NT / 16;
+    constexpr size_t most = sizeof(float) * (M * (192 + 4 + kLdP) + kTile * ((192 + 4) + (64 * NDV + 4)));
+    const cudaError_t e = allow_smem<latent_forward_f32_kernel<T, NDV, RI, NT>>(most);
     if (e != cudaSuccess) return e;
-    const size_t bytes = sizeof(float) * kTile * (2 * (a.Dk + a.Ds + 4) + (64 * NDV + 4) + kLdP);
-    const dim3 grid(tile_slots(a.total_q, a.num_seqs, kTile), a.H);
-    latent_forward_f32_kernel<T, NDV><<<grid, kThreads, bytes, s>>>(a);
+    const int ld = a.Dk + a.Ds + 4;
+    const size_t bytes = sizeof(float) * (M * (ld + kLdP) + kTile * (ld + (64 * NDV + 4)));
+    const dim3 grid(tile_slots(a.total_q, a.num_seqs, M), a.H);
+    latent_forward_f32_kernel<T, NDV, RI, NT><<<grid, NT, bytes, s>>>(a);
     return cudaGetLastError();
+}
+template <typename T, int NDV> cudaError_t forward_nv(const LatentArgs &a, cudaStream_t s) {
+    // fewer tiles of 64 rows than SMs: tiles of 16
+    const bool few = (long)(a.total_q / kTile + 1) * a.H < 148;
+    return few ? forward_ri<T, NDV, 1, 256>(a, s) : forward_ri<T, NDV, 4, 512>(a, s);
 }
 
 template <typename T, int ND, int NDV> cudaError_t backward_nd(const LatentArgs &a, cudaStream_t s) {
@@ -379,58 +393,88 @@ template <typename T> cudaError_t backward_t(const LatentArgs &a, cudaStream_t s
 // Absorbed form over pages.  One CTA per (split of a sequence, 16 query rows);
 // the splits' outputs and log-sum-exps are joined by a second kernel.
 // ---------------------------------------------------------------------------
-constexpr int kDecRows = 16, kDecTok = 32;
+constexpr int kDecTok = 32;
 
-template <typename T, int NL>      // Dl = 128 NL
-__global__ void __launch_bounds__(kThreads) latent_decode_f32_kernel(LatentDecodeArgs a, int splits) {
+// ROWS = 16 or 32 query rows a CTA, 16 threads each: 32 halve the reads of the
+// cache where there are that many.  The next tile's rows are copied (cp.async)
+// while this one is worked on.
+template <int NL, int ROWS>      // Dl = 128 NL
+__global__ void __launch_bounds__(16 * ROWS) latent_decode_f32_kernel(LatentDecodeArgs a, int splits) {
     extern __shared__ __align__(16) float smem[];
-    constexpr int Dl = 128 * NL;
+    using T = float;
+    constexpr int kThreads = 16 * ROWS;
+    __shared__ const T *row_s[2][kDecTok];
+    constexpr int Dl = 128 * NL, LP = kDecTok + 4;
     const int D = Dl + a.Ds, ld = D + 4;
-    float *Qs = smem, *Cs = Qs + kDecRows * ld, *Ps = Cs + kDecTok * ld, *stat = Ps + kDecRows * (kDecTok + 4);
-    // stat: rescaling factors of the tile [16]
-    const int b = blockIdx.x / splits, sp = blockIdx.x % splits, R = a.T * a.H, row0 = blockIdx.y * kDecRows;
-    const int rows = min(kDecRows, R - row0), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float *Qs = smem, *Cs0 = Qs + ROWS * ld, *Ps = Cs0 + 2 * kDecTok * ld, *stat = Ps + ROWS * LP;
+    // stat: rescaling factors of the tile [ROWS]
+    const int b = blockIdx.x / splits, sp = blockIdx.x % splits, R = a.T * a.H, row0 = blockIdx.y * ROWS;
+    const int rows = min(ROWS, R - row0), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long most = (long)a.table_width * a.page_size;
     const int given = a.lens[b];
     const int len = (int)min((long)max(given, 0), most);
     if ((given < 0 || given > most) && tid == 0) atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
     const int tiles = (len + kDecTok - 1) / kDecTok;
     const int t_lo = (int)((long)tiles * sp / splits), t_hi = (int)((long)tiles * (sp + 1) / splits);
-    for (int e = tid; e < kDecRows * D / 4; e += kThreads) {
-        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
-            const size_t row = (size_t)b * R + row0 + r;
-            x = c < Dl ? Io<T>::ld4((const T *)a.q + row * Dl + c) : Io<T>::ld4((const T *)a.q_shared + row * a.Ds + c - Dl);
-        }
-        *reinterpret_cast<float4 *>(Qs + r * ld + c) = x;
-    }
-    // scores: thread = 4 rows x 4 tokens over one of 8 slices of the columns
-    const int slice = lane & 7, blk = warp * 4 + (lane >> 3), br = (blk & 3) * 4, bt = (blk >> 2) * 4;
-    float m = -INFINITY, l = 0.f;                       // of row tid / 16 (16 threads each)
-    const int srow = tid >> 4, sc = tid & 15;
-    // outputs: thread = rows 8 (tid / 128) .. + 7, columns tid % 128 + 128 c
-    const int og = tid >> 7, oc = tid & 127;
-    float o[8][NL] = {};
-    for (int t = t_lo; t < t_hi; ++t) {
-        const int j0 = t * kDecTok;
-        __syncthreads();
-        for (int e = tid; e < kDecTok * D / 4; e += kThreads) {
-            const int r = e / (D / 4), c = (e % (D / 4)) * 4, j = j0 + r;
+    for (int r = warp; r < ROWS; r += kThreads / 32)
+        for (int c = 4 * lane; c < D; c += 128) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j < len) {
+            if (r < rows) {
+                const size_t row = (size_t)b * R + row0 + r;
+                x = c < Dl ? Io<T>::ld4((const T *)a.q + row * Dl + c) : Io<T>::ld4((const T *)a.q_shared + row * a.Ds + c - Dl);
+            }
+            *reinterpret_cast<float4 *>(Qs + r * ld + c) = x;
+        }
+    // scores: thread = 4 rows x 4 tokens over one of SL slices of the columns
+    constexpr int SL = kThreads / (ROWS / 4 * (kDecTok / 4));
+    const int slice = lane % SL, blk = warp * (32 / SL) + lane / SL, br = blk % (ROWS / 4) * 4, bt = blk / (ROWS / 4) * 4;
+    // softmax: PR threads a row, U tokens each
+    constexpr int PR = kThreads / ROWS, U = kDecTok / PR;
+    float m = -INFINITY, l = 0.f;
+    const int srow = tid / PR, sc = tid % PR;
+    // outputs: thread = rows RO (tid / 128) .., columns tid % 128 + 128 c
+    constexpr int RO = 8;
+    const int og = tid >> 7, oc = tid & 127;
+    float o[RO][NL] = {};
+    // where each token of tile t lies (null: not cached, or on a page outside the cache)
+    auto find = [&](int t) {
+        if (tid < kDecTok) {
+            const int j = t * kDecTok + tid;
+            const T *p = nullptr;
+            if (t < t_hi && j < len) {
                 const int page = a.table[(size_t)b * a.table_width + j / a.page_size];
                 if (page >= 0 && page < a.num_pages)
-                    x = Io<T>::ld4((const T *)a.pages + ((size_t)page * a.page_size + j % a.page_size) * D + c);
-                else if (c == 0)
+                    p = (const T *)a.pages + ((size_t)page * a.page_size + j % a.page_size) * D;
+                else
                     atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
             }
-            *reinterpret_cast<float4 *>(Cs + r * ld + c) = x;
+            row_s[t & 1][tid] = p;
         }
+    };
+    auto fetch = [&](int t) {
+        float *Cs = Cs0 + (t & 1) * kDecTok * ld;
+        for (int r = warp; r < kDecTok; r += kThreads / 32) {
+            const T *p = row_s[t & 1][r];
+            for (int c = 4 * lane; c < D; c += 128) {
+                if (p) cp_async16((uint32_t)__cvta_generic_to_shared(Cs + r * ld + c), p + c);
+                else *reinterpret_cast<float4 *>(Cs + r * ld + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        cp_async_commit();
+    };
+    find(t_lo);
+    __syncthreads();
+    if (t_lo < t_hi) fetch(t_lo);
+    for (int t = t_lo; t < t_hi; ++t) {
+        const int j0 = t * kDecTok;
+        const float *Cs = Cs0 + (t & 1) * kDecTok * ld;
+        find(t + 1);
+        cp_async_wait_all();
         __syncthreads();
+        if (t + 1 < t_hi) fetch(t + 1);
         {
             float s[4][4] = {};
-            for (int c = 4 * slice; c < D; c += 32) {
+            for (int c = 4 * slice; c < D; c += 4 * SL) {
                 float4 x[4], y[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -448,48 +492,42 @@ __global__ void __launch_bounds__(kThreads) latent_decode_f32_kernel(LatentDecod
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                    for (int off = 4; off; off >>= 1) s[i][j] += __shfl_xor_sync(0xffffffffu, s[i][j], off);
-                    if (slice == 0) Ps[(br + i) * (kDecTok + 4) + bt + j] = s[i][j];
+                    for (int off = SL / 2; off; off >>= 1) s[i][j] += __shfl_xor_sync(0xffffffffu, s[i][j], off);
+                    if (slice == 0) Ps[(br + i) * LP + bt + j] = s[i][j];
                 }
         }
         __syncthreads();
         {
-            // row srow by 16 threads of two tokens each
             const int last = len - a.T + (row0 + srow) / a.H;     // the last token this row sees
-            float x[2], top = m;
+            float x[U], top = m;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int j = j0 + sc + 16 * u;
-                bool on = j <= last && j < len && srow < rows;
-                if (on) {
-                    const int page = a.table[(size_t)b * a.table_width + j / a.page_size];
-                    on = page >= 0 && page < a.num_pages;
-                }
-                x[u] = on ? Ps[srow * (kDecTok + 4) + sc + 16 * u] * a.scale : -INFINITY;
+            for (int u = 0; u < U; ++u) {
+                const int i = sc + PR * u, j = j0 + i;
+                x[u] = j <= last && srow < rows && row_s[t & 1][i] ? Ps[srow * LP + i] * a.scale : -INFINITY;
                 top = fmaxf(top, x[u]);
             }
 #pragma unroll
-            for (int off = 8; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            for (int off = PR / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
             const float base = top == -INFINITY ? 0.f : top;
             const float keep = expf(m - base);
             m = top;
             l *= keep;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const float p = expf(x[u] - base);
                 l += p;
-                Ps[srow * (kDecTok + 4) + sc + 16 * u] = p;
+                Ps[srow * LP + sc + PR * u] = p;
             }
             if (sc == 0) stat[srow] = keep;
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float keep = stat[8 * og + i];
+        for (int i = 0; i < RO; ++i) {
+            const float keep = stat[RO * og + i];
 #pragma unroll
             for (int c = 0; c < NL; ++c) o[i][c] *= keep;
         }
-#pragma unroll 2
+#pragma unroll 1
         for (int j = 0; j < kDecTok; j += 4) {
             float y[4][NL];
 #pragma unroll
@@ -497,8 +535,8 @@ __global__ void __launch_bounds__(kThreads) latent_decode_f32_kernel(LatentDecod
 #pragma unroll
                 for (int c = 0; c < NL; ++c) y[u][c] = Cs[(j + u) * ld + oc + 128 * c];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 p = *reinterpret_cast<const float4 *>(Ps + (8 * og + i) * (kDecTok + 4) + j);
+            for (int i = 0; i < RO; ++i) {
+                const float4 p = *reinterpret_cast<const float4 *>(Ps + (RO * og + i) * LP + j);
 #pragma unroll
                 for (int c = 0; c < NL; ++c)
                     o[i][c] = fmaf(p.x, y[0][c], fmaf(p.y, y[1][c], fmaf(p.z, y[2][c], fmaf(p.w, y[3][c], o[i][c]))));
@@ -506,7 +544,7 @@ __global__ void __launch_bounds__(kThreads) latent_decode_f32_kernel(LatentDecod
         }
     }
 #pragma unroll
-    for (int off = 8; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    for (int off = PR / 2; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
     __syncthreads();
     if (sc == 0) {
         stat[srow] = l > 0.f ? 1.f / l : 0.f;
@@ -520,20 +558,19 @@ __global__ void __launch_bounds__(kThreads) latent_decode_f32_kernel(LatentDecod
     __syncthreads();
     float *po = a.part + (((size_t)a.B * R * splits + 3) & ~(size_t)3);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (8 * og + i >= rows) continue;
-        const size_t row = (size_t)b * R + row0 + 8 * og + i;
-        const float f = stat[8 * og + i];
+    for (int i = 0; i < RO; ++i) {
+        if (RO * og + i >= rows) continue;
+        const size_t row = (size_t)b * R + row0 + RO * og + i;
+        const float f = stat[RO * og + i];
 #pragma unroll
         for (int c = 0; c < NL; ++c) {
             if (splits > 1) po[(row * splits + sp) * Dl + oc + 128 * c] = o[i][c] * f;
-            else Io<T>::st((T *)a.out + row * Dl + oc + 128 * c, o[i][c] * f);
+            else static_cast<float *>(a.out)[row * Dl + oc + 128 * c] = o[i][c] * f;
         }
     }
 }
 
 // out = sum_s e^{lse_s - lse} o_s, lse = log sum_s e^{lse_s}: one CTA per row.
-template <typename T>
 __global__ void __launch_bounds__(128) latent_join_kernel(LatentDecodeArgs a, int splits) {
     const size_t row = blockIdx.x;
     const float *ls = a.part + row * splits;
@@ -550,37 +587,34 @@ __global__ void __launch_bounds__(128) latent_join_kernel(LatentDecodeArgs a, in
             const float4 y = *reinterpret_cast<const float4 *>(po + (size_t)s * a.Dl + c);
             x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
         }
-        Io<T>::st4((T *)a.out + row * a.Dl + c, x);
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * a.Dl + c) = x;
     }
     if (threadIdx.x == 0 && a.lse) a.lse[row] = sum > 0.f ? base + logf(sum) : -INFINITY;
 }
 
+int decode_rows(int rows) { return rows > 16 ? 32 : 16; }
 // Enough splits that two CTAs per SM have work, at most 64.
 int decode_splits(int B, int rows) {
-    const long units = (long)B * ((rows + kDecRows - 1) / kDecRows);
+    const int tile = decode_rows(rows);
+    const long units = (long)B * ((rows + tile - 1) / tile);
     const long want = (296 + units - 1) / units;
     return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
 }
 
-template <typename T, int NL> cudaError_t decode_nl(const LatentDecodeArgs &a, cudaStream_t s) {
-    constexpr size_t extra = kDecRows * (kDecTok + 4) + kDecRows;
-    constexpr size_t most = sizeof(float) * ((kDecRows + kDecTok) * (128 * NL + 64 + 4) + extra);
-    cudaError_t e = allow_smem<latent_decode_f32_kernel<T, NL>>(most);
+template <int NL, int ROWS> cudaError_t decode_rows_nl(const LatentDecodeArgs &a, cudaStream_t s) {
+    constexpr size_t extra = ROWS * (kDecTok + 4) + ROWS;
+    constexpr size_t most = sizeof(float) * ((ROWS + 2 * kDecTok) * (128 * NL + 64 + 4) + extra);
+    cudaError_t e = allow_smem<latent_decode_f32_kernel<NL, ROWS>>(most);
     if (e != cudaSuccess) return e;
     const int R = a.T * a.H, splits = decode_splits(a.B, R);
-    const size_t bytes = sizeof(float) * ((kDecRows + kDecTok) * (128 * NL + a.Ds + 4) + extra);
-    latent_decode_f32_kernel<T, NL><<<dim3(splits * a.B, (R + kDecRows - 1) / kDecRows), kThreads, bytes, s>>>(a, splits);
+    const size_t bytes = sizeof(float) * ((ROWS + 2 * kDecTok) * (128 * NL + a.Ds + 4) + extra);
+    latent_decode_f32_kernel<NL, ROWS><<<dim3(splits * a.B, (R + ROWS - 1) / ROWS), 16 * ROWS, bytes, s>>>(a, splits);
     if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
-    latent_join_kernel<T><<<a.B * R, 128, 0, s>>>(a, splits);
+    latent_join_kernel<<<a.B * R, 128, 0, s>>>(a, splits);
     return cudaGetLastError();
 }
-template <typename T> cudaError_t decode_t(const LatentDecodeArgs &a, cudaStream_t s) {
-    switch (a.Dl / 128) {
-        case 1: return decode_nl<T, 1>(a, s);
-        case 2: return decode_nl<T, 2>(a, s);
-        case 3: return decode_nl<T, 3>(a, s);
-        default: return decode_nl<T, 4>(a, s);
-    }
+template <int NL> cudaError_t decode_nl(const LatentDecodeArgs &a, cudaStream_t s) {
+    return decode_rows(a.T * a.H) == 32 ? decode_rows_nl<NL, 32>(a, s) : decode_rows_nl<NL, 16>(a, s);
 }
 
 }  // namespace
@@ -615,7 +649,12 @@ cudaError_t launch_latent_backward_f32(const LatentArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s) {
-    return decode_t<float>(a, s);
+    switch (a.Dl / 128) {
+        case 1: return decode_nl<1>(a, s);
+        case 2: return decode_nl<2>(a, s);
+        case 3: return decode_nl<3>(a, s);
+        default: return decode_nl<4>(a, s);
+    }
 }
 
 size_t latent_backward_scratch_bytes(int total_q, int total_k, int H, int Ds) {
