@@ -59,7 +59,7 @@ template <int NT> struct Small {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t q_full, q_empty, s_full[2], p_ready, pv_done, o_empty;
     uint64_t info[kInfo];
-    float wmax[2][4][NT];
+    float wmax[4][NT];
     float lsum[4][NT];
     float factor[NT];
     long long sums[kScan];
@@ -248,43 +248,42 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
                     }
                 }
             }
-            // the tile's maximum of each of my columns
-            float top[C][2];
+            // The rows' maxima are only looked for when some score passes the one in use by more than 2^kGrow: P
+            // stays in range, and a tile costs one barrier and no exchange.
+            bool above = false;
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float x = fmaxf(v[c][u], v[c][2 + u]);
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    top[c][u] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                }
-            if (lane < 4)
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    *reinterpret_cast<float2 *>(&S.wmax[it & 1][quad][c0 + 8 * c + col]) = make_float2(top[c][0], top[c][1]);
-            named_bar_sync(bar, 128);
-            bool grown = false;
+                for (int u = 0; u < 4; ++u) above |= v[c][u] - m[c][u & 1] > kGrow;
             float f[C][2];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float2 x[4];
+            for (int c = 0; c < C; ++c) f[c][0] = f[c][1] = 1.f;
+            const bool grown = named_bar_any(bar, 128, above);
+            if (grown) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<float2 *>(&S.wmax[it & 1][q][c0 + 8 * c + col]);
-                top[c][0] = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
-                top[c][1] = fmaxf(fmaxf(x[0].y, x[1].y), fmaxf(x[2].y, x[3].y));
+                for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float now = top[c][u];
-                    f[c][u] = 1.f;
-                    if (now > m[c][u] + kGrow || (m[c][u] == -INFINITY && now > -INFINITY)) {
-                        f[c][u] = ex2(m[c][u] - now);
-                        m[c][u] = now;
-                        grown = true;
+                    for (int u = 0; u < 2; ++u) {
+                        float x = fmaxf(v[c][u], v[c][2 + u]);
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        if (lane < 4) S.wmax[quad][c0 + 8 * c + col + u] = x;
                     }
-                }
+                named_bar_sync(bar, 128);
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int r = c0 + 8 * c + col + u;
+                        const float now = fmaxf(fmaxf(S.wmax[0][r], S.wmax[1][r]), fmaxf(S.wmax[2][r], S.wmax[3][r]));
+                        if (now > m[c][u]) {
+                            f[c][u] = ex2(m[c][u] - now);
+                            m[c][u] = now;
+                        }
+                    }
             }
-            const bool rescale = __any_sync(0xffffffffu, grown) && t != walk.t0;
+            const bool rescale = grown && t != walk.t0;
             // P^T, and my part of the sums
             uint32_t pk[C][2];
 #pragma unroll
