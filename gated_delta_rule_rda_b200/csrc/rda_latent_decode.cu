@@ -35,6 +35,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "rda_io.cuh"
 #include "rda_latent.h"
 #include "sm100_pipe.cuh"
 
@@ -54,11 +55,18 @@ constexpr int kInfo = 16;                // tiles whose masks are kept (the ring
 constexpr float kGrow = 8.f;             // rescale O when a maximum has grown by more (log2)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Columns of S^T (rows of the result) that the first four softmax warps take; four more take the rest.
+__host__ __device__ constexpr int split_cols(int nt) { return nt == 16 ? 16 : nt == 48 ? 32 : nt / 2; }
+__host__ __device__ constexpr int softmax_warps(int nt) { return nt == 16 ? 4 : 8; }
+// Warp 0 issues the MMAs, warps 1..4 copy the cache, then the softmax warps, the last one brings Q.
+constexpr int kCopyWarps = 4, kSoftWarp = 1 + kCopyWarps;
+__host__ __device__ constexpr int threads_of(int nt) { return 32 * (kSoftWarp + softmax_warps(nt) + 1); }
+
 // Shared memory behind the operand areas.
 template <int NT> struct Small {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t q_full, q_empty, s_full[2], p_ready, pv_done, o_empty;
-    uint64_t info[kInfo];
+    alignas(8) uint16_t seen[kInfo][kCopyWarps];    // which of a tile's tokens are cached, 16 by each copying warp
     float wmax[4][NT];
     float lsum[4][NT];
     float factor[NT];
@@ -78,7 +86,7 @@ struct Geometry {
 };
 
 struct Maps {
-    CUtensorMap pages, pages_shared, q, q_shared;
+    CUtensorMap q, q_shared;
 };
 
 __host__ __device__ inline uint32_t operand_bytes(int nt, int D, int pairs, int shared) {
@@ -103,8 +111,6 @@ __host__ __device__ inline Parts parts_of(float *base, const Geometry &g, int Dl
 struct Args {
     LatentDecodeArgs a;
     Geometry g;
-    int box_rows, chunks;                // rows and 64-column chunks of one copy
-    int pages_bound;                     // first page coordinate outside the map
 };
 
 // Tokens of sequence b (cut to what its table can hold).
@@ -156,16 +162,13 @@ __device__ __forceinline__ void store_result(uint32_t t_o, int NP, int rows, con
     }
 }
 
-// Columns of S^T (rows of the result) that the first four softmax warps take; four more take the rest.
-__host__ __device__ constexpr int split_cols(int nt) { return nt == 16 ? 16 : nt == 48 ? 32 : nt / 2; }
-__host__ __device__ constexpr int softmax_warps(int nt) { return nt == 16 ? 4 : 8; }
 
 template <int NT> struct SoftmaxCtx {
     Small<NT> &S;
     const Args &args;
     Walk walk;
     Waiter w;
-    uint8_t *pair_s, *p_s;
+    uint8_t *p_s;
     uint32_t tmem;
     int rt, grp, rows, row0;
     long long hi, total;
@@ -180,13 +183,12 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
     const Geometry &g = args.g;
     const Waiter w = x_.w;
     Walk walk = x_.walk;
-    uint8_t *pair_s = x_.pair_s, *p_s = x_.p_s;
-    const int NP = a.Dl / 128, NS = NP / g.sp, R = a.T * a.H;
+    uint8_t *p_s = x_.p_s;
+    const int NP = a.Dl / 128, R = a.T * a.H;
     const int rt = x_.rt, grp = x_.grp, row0 = x_.row0, rows = x_.rows;
     const long long hi = x_.hi, total = x_.total;
     const int c0 = half ? split_cols(NT) : 0, bar = 1 + half;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kSoft = 32 * softmax_warps(NT);
     const uint32_t t_o = x_.tmem + c0, t_s = x_.tmem + 4 * NT + c0;
     const int quad = warp & 3;                       // tokens 16 quad .. + 15 of a tile
     const int tok = lane >> 2, col = 2 * (lane & 3); // my tokens: tok, tok + 8; my columns: 8 c + col, + 1
@@ -220,33 +222,18 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) v[c][u] *= sc;       // log2 units; sc may be negative
-            const uint64_t valid = S.info[it % kInfo];
+            const uint2 seen = *reinterpret_cast<const uint2 *>(S.seen[it % kInfo]);
             const int j0 = t * kTok + 16 * quad + tok;
-            const bool whole = valid == ~0ull && t * kTok + kTok - 1 <= all_see;
+            const bool whole = (seen.x & seen.y) == 0xffffffffu && t * kTok + kTok - 1 <= all_see;
             if (!whole) {
-                const bool v0 = valid >> (16 * quad + tok) & 1, v1 = valid >> (16 * quad + tok + 8) & 1;
+                const uint32_t mine = (quad & 2 ? seen.y : seen.x) >> (16 * (quad & 1) + tok);
 #pragma unroll
                 for (int c = 0; c < C; ++c)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        if (!v0 || j0 > last[c][u]) v[c][u] = -INFINITY;
-                        if (!v1 || j0 + 8 > last[c][u]) v[c][2 + u] = -INFINITY;
+                        if (!(mine & 1) || j0 > last[c][u]) v[c][u] = -INFINITY;
+                        if (!(mine >> 8 & 1) || j0 + 8 > last[c][u]) v[c][2 + u] = -INFINITY;
                     }
-                // rows behind the sequence's end in a page may hold anything: 0 x NaN must not reach O
-                const int left = walk.len - t * kTok;
-                if (left < kTok) {
-                    const int from = max(left, 0);
-                    const int n = (min(kTok, (from + args.box_rows - 1) / args.box_rows * args.box_rows) - from) * 16;
-                    // the ring's slots are consecutive pairs of columns
-                    int pair = (int)((unsigned long long)it * NS % g.slots) * g.sp;
-                    for (int p = 0; p < NP; ++p) {
-                        uint8_t *base = pair_s + pair * kPair;
-                        for (int e = threadIdx.x - 64; e < n; e += kSoft)
-                            *reinterpret_cast<uint4 *>(base + ((e >> 3) & 1) * kBox + sw128(from + (e >> 4), e & 7)) =
-                                make_uint4(0, 0, 0, 0);
-                        if (++pair == g.slots * g.sp) pair = 0;
-                    }
-                }
             }
             // The rows' maxima are only looked for when some score passes the one in use by more than 2^kGrow: P
             // stays in range, and a tile costs one barrier and no exchange.
@@ -372,7 +359,7 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
         tc_fence_before();
         mbar_arrive(&S.o_empty);
         named_bar_sync(bar, 128);                                  // factors are free again
-        if (rt == 0 && threadIdx.x == 64 && walk.pos >= hi) {
+        if (rt == 0 && threadIdx.x == 32 * kSoftWarp && walk.pos >= hi) {
             // this group's last segment: does its sequence begin here and go on in others?
             int4 rec = make_int4(-1, 0, 0, 0);
             if (!done && walk.t0 == 0) {
@@ -390,7 +377,7 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
 }
 
 template <int NT>
-__global__ void __launch_bounds__(64 + 32 * softmax_warps(NT), 1) latent_decode_kernel(const __grid_constant__ Maps maps, const Args args) {
+__global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const __grid_constant__ Maps maps, const Args args) {
     extern __shared__ uint8_t smem_raw[];
     const LatentDecodeArgs &a = args.a;
     const Geometry &g = args.g;
@@ -410,7 +397,7 @@ __global__ void __launch_bounds__(64 + 32 * softmax_warps(NT), 1) latent_decode_
         tmem_relinquish();
     }
     if (tid == 32) {
-        for (int i = 0; i < g.slots; ++i) mbar_init(&S.full[i], 1), mbar_init(&S.empty[i], 1);
+        for (int i = 0; i < g.slots; ++i) mbar_init(&S.full[i], 32 * kCopyWarps), mbar_init(&S.empty[i], 1);
         mbar_init(&S.q_full, 1);
         mbar_init(&S.q_empty, 1);
         mbar_init(&S.s_full[0], 1);
@@ -420,7 +407,6 @@ __global__ void __launch_bounds__(64 + 32 * softmax_warps(NT), 1) latent_decode_
         mbar_init(&S.o_empty, 32 * softmax_warps(NT));
         S.abort = 0;
         fence_mbar_init();
-        prefetch_tensormap(&maps.pages);
         prefetch_tensormap(&maps.q);
     }
     // this group's range of the tiles of all sequences
@@ -483,97 +469,6 @@ __global__ void __launch_bounds__(64 + 32 * softmax_warps(NT), 1) latent_decode_
               a.B <= kLens ? S.lens : nullptr};
 
     if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        if (elect_one()) {
-            RingPos pr;
-            int sr = 0;
-            uint32_t seg = 0, it = 0;
-            const int ng = kTok / args.box_rows;           // row boxes of a tile: 1, 2 or 4
-            bool go = true;
-            int page_next[4];                              // of the tile that comes next, of this sequence or the next one
-            auto look_up = [&](const Walk &x, int t) {
-                const int32_t *table = a.table + (size_t)x.seq * a.table_width;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = t * kTok + i * args.box_rows;
-                    page_next[i] = i < ng && j < x.len ? table[j / a.page_size] : -1;
-                }
-            };
-            bool more = walk.next(a);
-            if (more) look_up(walk, walk.t0);
-            while (more) {
-                Walk after = walk;
-                const bool another = after.next(a);
-                for (int t = walk.t0; t < walk.t1; ++t, ++it) {
-                    // a page outside the cache, or behind the end: a coordinate outside the map (zeros)
-                    int row[4], page[4];
-                    uint64_t m = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = t * kTok + i * args.box_rows;
-                        row[i] = j % a.page_size;
-                        page[i] = page_next[i];
-                        if (page[i] >= 0 && page[i] < a.num_pages) {
-                            if (i < ng) m |= (args.box_rows == 64 ? ~0ull : (1ull << args.box_rows) - 1) << (i * args.box_rows);
-                        } else {
-                            if (i < ng && j < walk.len) atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
-                            page[i] = args.pages_bound;
-                        }
-                    }
-                    if (t + 1 < walk.t1) look_up(walk, t + 1);
-                    else if (another) look_up(after, after.t0);
-                    const int left = walk.len - t * kTok;
-                    if (left < kTok) m &= left <= 0 ? 0ull : (1ull << left) - 1;
-                    S.info[it % kInfo] = m;
-                    for (int n = 0; n < NS; ++n) {
-                        // The shared columns come with the tile's last slot; theirs is free once the scores that
-                        // read it last are done.
-                        const bool with = n == NS - 1 && a.Ds;
-                        if (with && it >= (uint32_t)g.shared)
-                            go = go && w.wait(&S.s_full[(it - g.shared) & 1], ((it - g.shared) >> 1) & 1);
-                        if (it * NS + n >= (uint32_t)g.slots) go = go && w.wait(&S.empty[pr.slot], pr.phase ^ 1);
-                        if (!go) break;
-                        uint64_t *full = &S.full[pr.slot];
-                        mbar_arrive_expect_tx(full, g.sp * kPair + (with ? kBox : 0));
-                        uint8_t *dst = pair_s + pr.slot * g.sp * kPair;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (i >= ng) continue;
-                            for (int x = 0; x < 2 * g.sp; x += args.chunks)
-                                tma_load_4d(dst + x * kBox + i * args.box_rows * 128, &maps.pages, full, 0, row[i],
-                                            n * 2 * g.sp + x, page[i]);
-                            if (with)
-                                tma_load_4d(shared_s + sr * kBox + i * args.box_rows * 128, &maps.pages_shared, full, 0,
-                                            row[i], a.Dl / 64, page[i]);
-                        }
-                        if (with && ++sr == g.shared) sr = 0;
-                        pr.next(g.slots);
-                        if (n == 0 && t == walk.t0) {
-                            // the segment's queries, once the scores of the one before are done
-                            go = seg == 0 || w.wait(&S.q_empty, (seg - 1) & 1);
-                            if (!go) break;
-                            mbar_arrive_expect_tx(&S.q_full, NB * NT * 128);
-                            const int r = walk.seq * R + row0;
-                            for (int c = 0; c < a.Dl / 64; ++c)
-                                tma_load_3d(q_s + c * NT * 128, &maps.q, &S.q_full, c * 64, r, 0);
-                            if (a.Ds) tma_load_3d(q_s + (NB - 1) * NT * 128, &maps.q_shared, &S.q_full, 0, r, 0);
-                            ++seg;
-                        }
-                    }
-                }
-                walk = after;
-                more = another;
-            }
-            if (S.abort) {
-                // copies in flight land before the CTA leaves: the last phase of every slot that was filled
-                // (one that never was counts as complete)
-                const uint64_t t0 = Waiter::now();
-                for (int i = 0; i < g.slots; ++i) w.drain(&S.full[i], (i < pr.slot ? pr.phase : pr.phase ^ 1), t0);
-                if (seg > 0) w.drain(&S.q_full, (seg - 1) & 1, t0);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         if (elect_one()) {
             RingPos qk_p, pv_p;
@@ -625,6 +520,7 @@ __global__ void __launch_bounds__(64 + 32 * softmax_warps(NT), 1) latent_decode_
                 uint32_t acc = 0;
                 for (int n = 0; n < NS; ++n) {
                     ok = arrived(&S.full[qk_p.slot], qk_p.phase) && ok;
+                    fence_proxy_async_smem();            // the copies wrote through the generic proxy
                     tc_fence_after();
                     if (ok) {
                         for (int p = 0; p < g.sp; ++p) {
@@ -665,12 +561,98 @@ __global__ void __launch_bounds__(64 + 32 * softmax_warps(NT), 1) latent_decode_
             if (S.abort && it > 0) w.drain(&S.pv_done, (it - 1) & 1, Waiter::now());
         }
         __syncwarp();
+    } else if (warp < kSoftWarp) {
+        // ------------------------------------------------------------ copies: 16 tokens of a tile each
+        // (pages are multiples of 16 tokens: a warp's tokens of a tile lie on one page)
+        const int mine = warp - 1;
+        RingPos pr;
+        int sr = 0;
+        uint32_t it = 0;
+        bool go = true;
+        auto page_of = [&](const Walk &x, int t) {
+            const int j = t * kTok + 16 * mine;
+            return j < x.len ? a.table[(size_t)x.seq * a.table_width + j / a.page_size] : -1;
+        };
+        bool more = walk.next(a);
+        int page_next = more ? page_of(walk, walk.t0) : -1;
+        const __nv_bfloat16 *pages = static_cast<const __nv_bfloat16 *>(a.pages);
+        const int D = a.Dl + a.Ds;
+        while (more) {
+            Walk after = walk;
+            const bool another = after.next(a);
+            for (int t = walk.t0; t < walk.t1; ++t, ++it) {
+                const int j = t * kTok + 16 * mine, page = page_next;
+                const bool ok = page >= 0 && page < a.num_pages;
+                if (t + 1 < walk.t1) page_next = page_of(walk, t + 1);
+                else if (another) page_next = page_of(after, after.t0);
+                // tokens behind the end, or on a page outside the cache: zeros, whatever the cache holds there
+                const int have = ok ? min(16, walk.len - j) : 0;
+                if (lane == 0) {
+                    if (!ok && j < walk.len) atomicCAS(a.err, 0, (int32_t)RDA_ERR_INVALID_ARG);
+                    S.seen[it % kInfo][mine] = (uint16_t)((1u << max(have, 0)) - 1);
+                }
+                const __nv_bfloat16 *src = ok ? pages + ((size_t)page * a.page_size + j % a.page_size) * D : static_cast<const __nv_bfloat16 *>(a.q);
+                for (int n = 0; n < NS; ++n) {
+                    // The shared columns come with the tile's last slot; theirs is free once the scores that read it
+                    // last are done.
+                    const bool with = n == NS - 1 && a.Ds;
+                    if (with && it >= (uint32_t)g.shared)
+                        go = w.wait(&S.s_full[(it - g.shared) & 1], ((it - g.shared) >> 1) & 1) && go;
+                    if (it * NS + n >= (uint32_t)g.slots) go = w.wait(&S.empty[pr.slot], pr.phase ^ 1) && go;
+                    const uint32_t dst = smem_u32(pair_s) + pr.slot * g.sp * kPair;
+                    if (g.sp == 2) {
+                        // 512 bytes of a row at a time
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            cp_async16_or_zero(dst + (lane >> 3) * kBox + sw128(16 * mine + r, lane & 7),
+                                               src + (size_t)min(r, max(have - 1, 0)) * D + n * 256 + lane * 8, r < have ? 16 : 0);
+                    } else {
+                        const int half = lane >> 4, x = lane & 15;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 2 * i + half;
+                            cp_async16_or_zero(dst + (x >> 3) * kBox + sw128(16 * mine + r, x & 7),
+                                               src + (size_t)min(r, max(have - 1, 0)) * D + n * 128 + x * 8, r < have ? 16 : 0);
+                        }
+                    }
+                    if (with) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 4 * i + (lane >> 3);
+                            cp_async16_or_zero(smem_u32(shared_s) + sr * kBox + sw128(16 * mine + r, lane & 7),
+                                               src + (size_t)min(r, max(have - 1, 0)) * D + a.Dl + (lane & 7) * 8, r < have ? 16 : 0);
+                        }
+                        if (++sr == g.shared) sr = 0;
+                    }
+                    cp_async_arrive(smem_u32(&S.full[pr.slot]));
+                    pr.next(g.slots);
+                }
+            }
+            walk = after;
+            more = another;
+        }
+        cp_async_wait_all();                                // nothing lands after the CTA has left
+    } else if (warp == kSoftWarp + softmax_warps(NT)) {
+        // ------------------------------------------------------------ Q of each segment, once the one before is used up
+        if (elect_one()) {
+            uint32_t seg = 0;
+            while (walk.next(a)) {
+                if (seg > 0 && !w.wait(&S.q_empty, (seg - 1) & 1)) break;
+                mbar_arrive_expect_tx(&S.q_full, NB * NT * 128);
+                const int r = walk.seq * R + row0;
+                for (int c = 0; c < a.Dl / 64; ++c) tma_load_3d(q_s + c * NT * 128, &maps.q, &S.q_full, c * 64, r, 0);
+                if (a.Ds) tma_load_3d(q_s + (NB - 1) * NT * 128, &maps.q_shared, &S.q_full, 0, r, 0);
+                ++seg;
+            }
+            if (S.abort && seg > 0) w.drain(&S.q_full, (seg - 1) & 1, Waiter::now());
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        const SoftmaxCtx<NT> x{S, args, walk, w, pair_s, p_s, tmem, rt, grp, rows, row0, hi, total};
-        if (warp < 6) softmax<NT, split_cols(NT)>(x, 0);
+        const SoftmaxCtx<NT> x{S, args, walk, w, p_s, tmem, rt, grp, rows, row0, hi, total};
+        if (warp < kSoftWarp + 4) softmax<NT, split_cols(NT)>(x, 0);
         else if constexpr (NT > 16) softmax<NT, NT - split_cols(NT)>(x, 1);
-        if (rt == 0 && tid == 64 && lo >= hi) parts_of(a.part, g, a.Dl).rec[grp] = make_int4(-1, 0, 0, 0);
+        if (rt == 0 && tid == 32 * kSoftWarp && lo >= hi) parts_of(a.part, g, a.Dl).rec[grp] = make_int4(-1, 0, 0, 0);
     }
     tc_fence_before();
     __syncthreads();
@@ -766,7 +748,7 @@ static_assert(sizeof(Small<64>) % 8 == 0, "barriers are 8-byte aligned");
 template <int NT> cudaError_t launch(const Maps &maps, const Args &args, cudaStream_t s) {
     cudaError_t e = allow_smem<latent_decode_kernel<NT>>(232448);
     if (e != cudaSuccess) return e;
-    latent_decode_kernel<NT><<<args.g.rt * args.g.groups, 64 + 32 * softmax_warps(NT), args.g.smem, s>>>(maps, args);
+    latent_decode_kernel<NT><<<args.g.rt * args.g.groups, threads_of(NT), args.g.smem, s>>>(maps, args);
     return cudaGetLastError();
 }
 
@@ -781,20 +763,11 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s) {
     Args args{};
     args.a = a;
     args.g = geometry(a.T, a.H, a.Dl, a.Ds);
-    args.box_rows = std::min(kTok, a.page_size & -a.page_size);
-    const int D = a.Dl + a.Ds, R = a.T * a.H;
+    const int R = a.T * a.H;
     if (args.g.slots * args.g.sp < 2 * (a.Dl / 128)) return cudaErrorInvalidConfiguration;
     Maps maps;
     std::memset(&maps, 0, sizeof(maps));
-    // without a page the map is never read inside its bounds; any aligned base will do
-    const int pages = std::max(1, a.num_pages);
-    args.pages_bound = pages;
-    const void *base = a.num_pages ? a.pages : a.q;
-    // one copy brings all chunks of a row box where it fills a tile's rows; smem keeps [chunk][row][64]
-    args.chunks = args.box_rows == kTok ? 2 * args.g.sp : 1;
-    if (!make_map_pages(&maps.pages, base, D, a.page_size, pages, args.box_rows, args.chunks) ||
-        !make_map_pages(&maps.pages_shared, base, D, a.page_size, pages, args.box_rows, 1) ||
-        !make_map_3d(&maps.q, a.q, a.Dl, (uint64_t)a.B * R, 1, a.Dl, (uint64_t)a.B * R * a.Dl, args.g.nt, 1) ||
+    if (!make_map_3d(&maps.q, a.q, a.Dl, (uint64_t)a.B * R, 1, a.Dl, (uint64_t)a.B * R * a.Dl, args.g.nt, 1) ||
         (a.Ds && !make_map_3d(&maps.q_shared, a.q_shared, a.Ds, (uint64_t)a.B * R, 1, a.Ds, (uint64_t)a.B * R * a.Ds,
                               args.g.nt, 1)))
         return cudaErrorInvalidValue;
