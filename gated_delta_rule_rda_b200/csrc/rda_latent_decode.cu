@@ -65,7 +65,7 @@ __host__ __device__ constexpr int threads_of(int nt) { return 32 * (kSoftWarp + 
 // Shared memory behind the operand areas.
 template <int NT> struct Small {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
-    uint64_t q_full, q_empty, s_full[2], p_ready, pv_done, o_empty;
+    uint64_t q_full, q_empty, s_full[2], p_ready, pv_done, o_empty, drained;
     alignas(8) uint16_t seen[kInfo][kCopyWarps];    // which of a tile's tokens are cached, 16 by each copying warp
     float wmax[4][NT];
     float lsum[4][NT];
@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
         mbar_init(&S.s_full[1], 1);
         mbar_init(&S.p_ready, 32 * softmax_warps(NT));
         mbar_init(&S.pv_done, 1);
+        mbar_init(&S.drained, 1);
         mbar_init(&S.o_empty, 32 * softmax_warps(NT));
         S.abort = 0;
         fence_mbar_init();
@@ -471,8 +472,9 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
     if (warp == 0) {
         // ------------------------------------------------------------ MMAs
         if (elect_one()) {
-            RingPos qk_p, pv_p;
-            int qk_s = 0;
+            // One loop that issues whatever can go next: a slot's share of the scores once its copy has landed, a
+            // tile's values once softmax has left P.  Each is written out once and in short loops: the code of all
+            // roles has to stay in the instruction caches for the MMAs to be issued as fast as they run.
             constexpr uint32_t idS = idesc_bf16(kTok, NT, 0, 0), idO = idesc_bf16(128, NT, 1, 0);
             // descriptors count in units of 16 bytes: offsets are added to the first slot's
             const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024, kSw128), dp = smem_desc(smem_u32(p_s), 16, 1024, kSw128);
@@ -481,84 +483,81 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
             const uint64_t ds = smem_desc(smem_u32(shared_s), 16, 1024, kSw128);
             constexpr uint32_t kQBox = NT * 8, kPairD = kPair / 16, kBoxD = kBox / 16;
             const uint32_t slot_d = g.sp * kPairD;
-            Walk ahead = walk;                    // the scores run one tile ahead
-            bool more = ahead.next(a), owed = false;
-            int at = more ? ahead.t0 : 0, t = 0;
-            uint32_t qk_seg = 0, pv_seg = 0, it = 0, qk_it = 0;
-            // O^T += L^T P^T of tile t, once P is there
-            auto values = [&](bool ok) {
-                if (t == walk.t0 && pv_seg > 0) ok = w.wait(&S.o_empty, (pv_seg - 1) & 1) && ok;
-                tc_fence_after();
-                for (int n = 0; n < NS; ++n) {
-                    if (ok) {
-                        for (int p = 0; p < g.sp; ++p)
+            RingPos qk_p, pv_p;
+            int qk_shared = 0, part = 0;                 // slot of the shared columns; slots of the tile already issued
+            Walk ahead = walk;                           // the scores run up to one tile ahead of the values
+            bool more = ahead.next(a), left = walk.next(a);
+            int at = ahead.t0, t = walk.t0;
+            uint32_t qk_it = 0, qk_seg = 0, it = 0, seg = 0;
+            uint64_t since = 0;
+            uint32_t idle = 0;
+            while (left) {
+                if (qk_it > it && mbar_test(&S.p_ready, it & 1) && (t != walk.t0 || seg == 0 || mbar_test(&S.o_empty, (seg - 1) & 1))) {
+                    // O^T += L^T P^T of tile t
+                    tc_fence_after();
+                    for (int n = 0; n < NS; ++n) {
+                        for (int p = 0; p < g.sp; ++p) {
+                            const uint64_t da = dv + (pv_p.slot * slot_d + p * kPairD);
+                            const uint32_t d = t_o + (n * g.sp + p) * NT;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16(t_o + (n * g.sp + p) * NT, dv + (pv_p.slot * slot_d + p * kPairD + k * 128),
-                                         dp + k * 2, idO, t != walk.t0 || k > 0);
+                            for (int k = 0; k < 4; ++k) mma_bf16(d, da + k * 128, dp + k * 2, idO, t != walk.t0 || k > 0);
+                        }
                         mma_commit(&S.empty[pv_p.slot]);
+                        pv_p.next(g.slots);
                     }
-                    pv_p.next(g.slots);
-                }
-                mma_commit(&S.pv_done);
-                owed = false;
-            };
-            // Waits for operands of the next tile's scores; this tile's values go out in the meantime as soon
-            // as softmax is done, so that their slots are free again early.
-            auto arrived = [&](uint64_t *bar, uint32_t parity) {
-                if (mbar_test(bar, parity)) return true;
-                while (owed && !S.abort) {
-                    if (mbar_test(&S.p_ready, it & 1)) values(true);
-                    if (mbar_test(bar, parity)) return true;
-                }
-                return w.wait(bar, parity);
-            };
-            auto scores = [&]() {
-                // S^T of tile `at` of the segment `ahead`
-                bool ok = at != ahead.t0 || arrived(&S.q_full, qk_seg & 1);
-                const uint32_t d = t_s + (qk_it & 1) * NT;
-                uint32_t acc = 0;
-                for (int n = 0; n < NS; ++n) {
-                    ok = arrived(&S.full[qk_p.slot], qk_p.phase) && ok;
+                    mma_commit(&S.pv_done);
+                    ++it;
+                    if (++t == walk.t1) {
+                        ++seg;
+                        left = walk.next(a);
+                        t = walk.t0;
+                    }
+                    idle = 0;
+                } else if (more && qk_it < it + 2 && mbar_test(&S.full[qk_p.slot], qk_p.phase) &&
+                           (part > 0 || at != ahead.t0 || mbar_test(&S.q_full, qk_seg & 1))) {
+                    // S^T of tile `at` of the segment `ahead`: the columns of one slot
                     fence_proxy_async_smem();            // the copies wrote through the generic proxy
                     tc_fence_after();
-                    if (ok) {
-                        for (int p = 0; p < g.sp; ++p) {
-                            const uint64_t da = dc + (qk_p.slot * slot_d + p * kPairD), db = dq + (n * g.sp + p) * 2 * kQBox;
+                    const uint32_t d = t_s + (qk_it & 1) * NT;
+                    const uint64_t da = dc + qk_p.slot * slot_d, db = dq + part * 2 * g.sp * kQBox;
+                    for (int c = 0; c < 2 * g.sp; ++c)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                mma_bf16(d, da + ((k >> 2) * kBoxD + (k & 3) * 2), db + ((k >> 2) * kQBox + (k & 3) * 2), idS, acc);
-                                acc = 1;
-                            }
-                        }
-                        if (n == NS - 1 && a.Ds)
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(d, da + (c * kBoxD + k * 2), db + (c * kQBox + k * 2), idS, part > 0 || c > 0 || k > 0);
+                    qk_p.next(g.slots);
+                    if (++part == NS) {
+                        if (a.Ds) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_bf16(d, ds + (qk_s * kBoxD + k * 2), dq + (2 * NP * kQBox + k * 2), idS, 1);
+                                mma_bf16(d, ds + (qk_shared * kBoxD + k * 2), dq + (2 * NP * kQBox + k * 2), idS, 1);
+                            if (++qk_shared == g.shared) qk_shared = 0;
+                        }
+                        mma_commit(&S.s_full[qk_it & 1]);
+                        part = 0;
+                        ++qk_it;
+                        if (++at == ahead.t1) {
+                            mma_commit(&S.q_empty);
+                            ++qk_seg;
+                            more = ahead.next(a);
+                            at = ahead.t0;
+                        }
                     }
-                    qk_p.next(g.slots);
+                    idle = 0;
+                } else if ((++idle & 255) == 0) {
+                    // nothing for a while: give up when another role has, or after the limit
+                    if (S.abort) break;
+                    if (idle == 256) since = Waiter::now();
+                    else if (Waiter::now() - since > a.wait_ns) {
+                        S.abort = 1;
+                        atomicCAS(a.err, 0, (int32_t)RDA_ERR_TIMEOUT);
+                    }
                 }
-                if (++qk_s == g.shared) qk_s = 0;
-                mma_commit(&S.s_full[qk_it & 1]);
-                ++qk_it;
-                if (++at == ahead.t1) {
-                    mma_commit(&S.q_empty);
-                    ++qk_seg;
-                    more = ahead.next(a);
-                    at = ahead.t0;
-                }
-            };
-            if (more) scores();
-            while (walk.next(a)) {
-                for (t = walk.t0; t < walk.t1; ++t, ++it) {
-                    owed = true;
-                    if (more) scores();
-                    if (owed) values(w.wait(&S.p_ready, it & 1));
-                }
-                ++pv_seg;
             }
-            // every MMA has completed when pv_done has (the softmax warps wait for it, or below)
-            if (S.abort && it > 0) w.drain(&S.pv_done, (it - 1) & 1, Waiter::now());
+            if (S.abort) {
+                // what was issued completes before the CTA leaves
+                mma_commit(&S.drained);
+                w.drain(&S.drained, 0, Waiter::now());
+            }
         }
         __syncwarp();
     } else if (warp < kSoftWarp) {
@@ -602,18 +601,21 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
                     const uint32_t dst = smem_u32(pair_s) + pr.slot * g.sp * kPair;
                     if (g.sp == 2) {
                         // 512 bytes of a row at a time
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            cp_async16_or_zero(dst + (lane >> 3) * kBox + sw128(16 * mine + r, lane & 7),
-                                               src + (size_t)min(r, max(have - 1, 0)) * D + n * 256 + lane * 8, r < have ? 16 : 0);
-                    } else {
-                        const int half = lane >> 4, x = lane & 15;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 2 * i + half;
-                            cp_async16_or_zero(dst + (x >> 3) * kBox + sw128(16 * mine + r, x & 7),
-                                               src + (size_t)min(r, max(have - 1, 0)) * D + n * 128 + x * 8, r < have ? 16 : 0);
+                        const __nv_bfloat16 *x = src + n * 256 + lane * 8;
+                        const uint32_t to = dst + (lane >> 3) * kBox + 16 * mine * 128;
+                        if (have == 16) {
+#pragma unroll 8
+                            for (int r = 0; r < 16; ++r, x += D) cp_async16(to + sw128(r, lane & 7), x);
+                        } else {
+#pragma unroll 4
+                            for (int r = 0; r < 16; ++r, x += r < have ? D : 0)
+                                cp_async16_or_zero(to + sw128(r, lane & 7), x, r < have ? 16 : 0);
                         }
+                    } else {
+                        const int half = lane >> 4, y = lane & 15;
+                        for (int r = half; r < 16; r += 2)
+                            cp_async16_or_zero(dst + (y >> 3) * kBox + sw128(16 * mine + r, y & 7),
+                                               src + (size_t)min(r, max(have - 1, 0)) * D + n * 128 + y * 8, r < have ? 16 : 0);
                     }
                     if (with) {
 #pragma unroll
