@@ -437,6 +437,14 @@ def _need_like(t, name, shape, dtype, dev):
     raise ValueError(f"rda: {name} must be contiguous")
 
 
+def _device_of(t):
+    """Number of the CUDA device that holds ``t``."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("rda: tensors must be CUDA tensors (no CPU path exists)")
+    return dev
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -450,18 +458,25 @@ def _scratch(workspace, dev):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+# the current stream's handle without making a Stream object of it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _launch(fn, dev, stream, *args):
     """Calls a library function on CUDA device number ``dev`` (its current stream unless one is
     given), whatever device is current."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        handle = _current_stream(dev)
     elif stream.device_index != dev:
         raise ValueError(f"rda: the stream belongs to device {stream.device_index}, the tensors to {dev}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        code = fn(*args, stream.cuda_stream)
+        code = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, stream.cuda_stream)
+            code = fn(*args, handle)
     if code:
         raise RdaError(code, fn.__name__)
 
@@ -475,7 +490,7 @@ def _latent_sizes(q, k, v, q_shared, k_shared, cu_q, cu_k):
     total_q, H, Dk = q.shape
     total_k, Dv = k.shape[0], v.shape[2]
     Ds = 0 if k_shared is None else k_shared.shape[-1]
-    dev, dt = q.get_device(), q.dtype
+    dev, dt = _device_of(q), q.dtype
     _dtype_code(q)
     _need_like(q, "q", (total_q, H, Dk), dt, dev)
     _need_like(k, "k", (total_k, H, Dk), dt, dev)
@@ -506,7 +521,7 @@ def rda_latent_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, scale, q_sha
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     total_q, total_k, H, Dk, Ds, Dv, N = sizes = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
-    dev = q.get_device()
+    dev = _device_of(q)
     if out is None:
         out = q.new_empty((total_q, H, Dv))
     else:
@@ -532,7 +547,7 @@ def rda_latent_backward(q, k, v, out, lse, d_out, cu_seqlens_q, cu_seqlens_k=Non
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     total_q, total_k, H, Dk, Ds, Dv, N = sizes = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
-    dev = q.get_device()
+    dev = _device_of(q)
     _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
     _need_like(d_out, "d_out", (total_q, H, Dv), q.dtype, dev)
     _need_like(lse, "lse", (total_q, H), torch.float32, dev)
@@ -562,7 +577,7 @@ def rda_latent_decode(q, pages, block_table, seq_lens, *, scale, q_shared=None, 
     B, T, H, Dl = q.shape
     num_pages, page_size, D = pages.shape
     Ds = 0 if q_shared is None else q_shared.shape[-1]
-    dev, dt = q.get_device(), q.dtype
+    dev, dt = _device_of(q), q.dtype
     code = _dtype_code(q)
     _need_like(q, "q", (B, T, H, Dl), dt, dev)
     if q_shared is not None:
@@ -598,7 +613,7 @@ def rda_verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, nu
         raise ValueError("rda: draft_tokens is [B, T], target_probs [B, T + 1, V]")
     B, T = draft_tokens.shape
     V = target_probs.shape[2]
-    dev = target_probs.get_device()
+    dev = _device_of(target_probs)
     _need_like(draft_tokens, "draft_tokens", (B, T), torch.int32, dev)
     _need_like(target_probs, "target_probs", (B, T + 1, V), torch.float32, dev)
     _need_like(uniforms, "uniforms", (B, T + 1), torch.float32, dev)

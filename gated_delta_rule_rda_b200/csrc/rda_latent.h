@@ -65,7 +65,7 @@ struct VerifyArgs {
     const int32_t *num_drafts;   // [B] or null
     int32_t *tokens, *num_accepted;
     int B, T, V;
-    double2 *part;               // workspace: sums of the weights per slice
+    double *part;                // workspace: sums of the weights per slice
 };
 
 // Most drafted tokens one verification takes per sequence (one warp lane each).

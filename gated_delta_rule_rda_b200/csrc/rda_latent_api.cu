@@ -188,7 +188,7 @@ rda_status_t rda_verify_drafts(const int32_t *draft_tokens, const float *draft_p
     a.draft = draft_tokens; a.draft_probs = draft_probs; a.target_probs = target_probs; a.uniforms = uniforms;
     a.num_drafts = num_drafts; a.tokens = tokens; a.num_accepted = num_accepted;
     a.B = B; a.T = T; a.V = V;
-    a.part = reinterpret_cast<double2 *>(static_cast<uint8_t *>(workspace) + kErrorWordBytes);
+    a.part = reinterpret_cast<double *>(static_cast<uint8_t *>(workspace) + kErrorWordBytes);
     return done(launch_verify(a, static_cast<cudaStream_t>(stream)));
 }
 

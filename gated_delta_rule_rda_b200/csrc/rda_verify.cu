@@ -60,10 +60,52 @@ __device__ __forceinline__ Rows weight_rows(const VerifyArgs &a, int b, int k, i
     r.x = k < n && !a.draft_probs ? a.draft[(size_t)b * a.T + k] : -1;
     return r;
 }
-// (residual weight, weight of the target alone); written so that NaN weighs nothing
-__device__ __forceinline__ double2 weight(float p, float q, bool at_x) {
-    const double d = (double)p - (double)q;
-    return make_double2(!at_x && d > 0.0 ? d : 0.0, p > 0.f ? (double)p : 0.0);
+// A token's weight: max(p - q, 0), exact in fp64.  Without q the target's own; 0 at the point mass.  A comparison of
+// the floats decides, so that NaN weighs nothing and only what counts is converted.
+__device__ __forceinline__ double weight(float p, float q, bool at_x) {
+    return p > q && !at_x ? (double)p - (double)q : 0.0;
+}
+// Sum of slice s by a warp (every lane gets it), all its loads in flight at once.
+template <bool VEC> __device__ __forceinline__ double slice_sum(const Rows &r, int s, int V, int lane) {
+    const int i0 = s * kSlice;
+    double sum = 0.0;
+    if (VEC) {
+        float4 p[8], q[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + 128 * u + 4 * lane;
+            p[u] = q[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < V) {
+                p[u] = __ldg(reinterpret_cast<const float4 *>(r.p + i));
+                if (r.q) q[u] = __ldg(reinterpret_cast<const float4 *>(r.q + i));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + 128 * u + 4 * lane;
+            sum += weight(p[u].x, q[u].x, i == r.x);
+            sum += weight(p[u].y, q[u].y, i + 1 == r.x);
+            sum += weight(p[u].z, q[u].z, i + 2 == r.x);
+            sum += weight(p[u].w, q[u].w, i + 3 == r.x);
+        }
+    } else {
+        // rows of a vocabulary that is no multiple of 4 start anywhere: single floats
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            float p[16], q[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int i = i0 + 512 * half + 32 * u + lane;
+                p[u] = i < V ? __ldg(r.p + i) : 0.f;
+                q[u] = r.q && i < V ? __ldg(r.q + i) : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 16; ++u) sum += weight(p[u], q[u], i0 + 512 * half + 32 * u + lane == r.x);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    return sum;
 }
 
 template <bool VEC>
@@ -71,58 +113,13 @@ __global__ void __launch_bounds__(32 * kWarps) verify_sums_kernel(VerifyArgs a) 
     const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ptx::pdl_launch_dependents();
     int n;
-    int k = kept_drafts(a, b, lane, &n);
+    const int k = kept_drafts(a, b, lane, &n);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.num_accepted[b] = k;
     const Rows r = weight_rows(a, b, k, n);
     const int ns = slices_of(a.V);
     for (int s = blockIdx.x * kWarps + warp; s < ns; s += gridDim.x * kWarps) {
-        const int i0 = s * kSlice;
-        double rest = 0.0, all = 0.0;
-        if (VEC) {
-            float4 p[8], q[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int i = i0 + 128 * u + 4 * lane;
-                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                p[u] = i < a.V ? __ldg(reinterpret_cast<const float4 *>(r.p + i)) : z;
-                q[u] = r.q && i < a.V ? __ldg(reinterpret_cast<const float4 *>(r.q + i)) : z;
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int i = i0 + 128 * u + 4 * lane;
-                const float ps[4] = {p[u].x, p[u].y, p[u].z, p[u].w}, qs[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const double2 w = weight(ps[v], qs[v], i + v == r.x);
-                    rest += w.x;
-                    all += w.y;
-                }
-            }
-        } else {
-            // rows of a vocabulary that is no multiple of 4 start anywhere: single floats
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float p[16], q[16];
-#pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    const int i = i0 + 512 * half + 32 * u + lane;
-                    p[u] = i < a.V ? __ldg(r.p + i) : 0.f;
-                    q[u] = r.q && i < a.V ? __ldg(r.q + i) : 0.f;
-                }
-#pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    const double2 w = weight(p[u], q[u], i0 + 512 * half + 32 * u + lane == r.x);
-                    rest += w.x;
-                    all += w.y;
-                }
-            }
-        }
-#pragma unroll
-        for (int off = 16; off; off >>= 1) {
-            rest += __shfl_xor_sync(0xffffffffu, rest, off);
-            all += __shfl_xor_sync(0xffffffffu, all, off);
-        }
-        if (lane == 0) a.part[(size_t)b * ns + s] = make_double2(rest, all);
+        const double sum = slice_sum<VEC>(r, s, a.V, lane);
+        if (lane == 0) a.part[(size_t)b * ns + s] = sum;
     }
 }
 
@@ -149,89 +146,88 @@ __device__ __forceinline__ double block_scan(double x, double *warp_s, double *t
 
 __global__ void __launch_bounds__(kPick) verify_pick_kernel(VerifyArgs a) {
     __shared__ double warp_s[kPick / 32], start_s;
-    __shared__ int slice_s, last_s, token_s;
+    __shared__ int slice_s, last_s, token_s, tail_s;
     const int b = blockIdx.x, tid = threadIdx.x;
-    if (tid == 0) slice_s = 0x7fffffff, last_s = -1, token_s = 0x7fffffff, start_s = 0.0;
+    if (tid == 0) slice_s = token_s = 0x7fffffff, last_s = tail_s = -1, start_s = 0.0;
     const int n = a.num_drafts ? min(max(a.num_drafts[b], 0), a.T) : a.T;
     const double u = a.uniforms[(size_t)b * (a.T + 1) + a.T];
     const int ns = slices_of(a.V);
-    const double2 *part = a.part + (size_t)b * ns;
+    double *part = a.part + (size_t)b * ns;
     ptx::pdl_wait_primary();
     const int k = a.num_accepted[b];
-    const Rows r = weight_rows(a, b, k, n);
-    // the residual's sum, the target's
-    double rest = 0.0, all = 0.0;
-    for (int s = tid; s < ns; s += kPick) {
-        const double2 w = part[s];
-        rest += w.x;
-        all += w.y;
+    Rows r = weight_rows(a, b, k, n);
+    // each thread's slices are consecutive: one scan gives every slice's start
+    const int per = (ns + kPick - 1) / kPick, s0 = min(ns, tid * per), s1 = min(ns, s0 + per);
+    double mine, end, total;
+    for (int pass = 0;; ++pass) {
+        mine = 0.0;
+        for (int s = s0; s < s1; ++s) mine += part[s];
+        end = block_scan(mine, warp_s, &total);
+        if (total > 0.0 || pass || (!r.q && r.x < 0)) break;
+        // a residual of nothing (the target nowhere above the draft): the target itself
+        r.q = nullptr;
+        r.x = -1;
+        for (int s = tid >> 5; s < ns; s += kPick / 32) {
+            const double sum = slice_sum<false>(r, s, a.V, tid & 31);
+            if ((tid & 31) == 0) part[s] = sum;
+        }
+        __syncthreads();
     }
-    double total_rest, total_all;
-    block_scan(rest, warp_s, &total_rest);
-    block_scan(all, warp_s, &total_all);
-    // a residual of nothing (the target nowhere above the draft): the target itself
-    const bool residual = k < n && total_rest > 0.0;
-    const double goal = u * (residual ? total_rest : total_all);
+    const double goal = u * total;
+    double upto = end - mine;
     // the first slice whose end passes the goal
-    double done = 0.0;
-    for (int s0 = 0; s0 < ns; s0 += kPick) {
-        const int s = s0 + tid;
-        const double2 w2 = s < ns ? part[s] : make_double2(0.0, 0.0);
-        const double w = residual ? w2.x : w2.y;
-        double sum;
-        const double upto = done + block_scan(w, warp_s, &sum);
+    for (int s = s0; s < s1; ++s) {
+        const double w = part[s];
+        upto += w;
         if (w > 0.0) {
             if (upto > goal) atomicMin(&slice_s, s);
             atomicMax(&last_s, s);
         }
-        __syncthreads();
-        if (s == slice_s) start_s = upto - w;
-        done += sum;
-        __syncthreads();
-        if (slice_s != 0x7fffffff) break;
     }
+    __syncthreads();
     // none passes it (u next to 1, and rounding): the last one that weighs anything
     const bool past = slice_s == 0x7fffffff;
     const int slice = past ? last_s : slice_s;
-    const double start = start_s;
-    __syncthreads();
-    if (tid == 0) last_s = -1;
+    if (slice >= s0 && slice < s1) {
+        double start = end - mine;
+        for (int s = s0; s < slice; ++s) start += part[s];
+        start_s = start;
+    }
     double w[4] = {0.0, 0.0, 0.0, 0.0};
     const int i0 = slice * kSlice + 4 * tid;
     if (slice >= 0) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int i = i0 + v;
-            if (i < a.V) {
-                const double2 x = weight(r.p[i], r.q ? r.q[i] : 0.f, i == r.x);
-                w[v] = residual ? x.x : x.y;
-            }
+            if (i < a.V) w[v] = weight(r.p[i], r.q ? r.q[i] : 0.f, i == r.x);
         }
     }
+    const double four = w[0] + w[1] + w[2] + w[3];
     double sum;
-    double upto = start + block_scan(w[0] + w[1] + w[2] + w[3], warp_s, &sum) - (w[0] + w[1] + w[2] + w[3]);
+    double at = block_scan(four, warp_s, &sum) - four + start_s;      // its barriers publish start_s
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-        upto += w[v];
+        at += w[v];
         if (w[v] > 0.0) {
-            if (!past && upto > goal) atomicMin(&token_s, i0 + v);
-            atomicMax(&last_s, i0 + v);
+            if (!past && at > goal) atomicMin(&token_s, i0 + v);
+            atomicMax(&tail_s, i0 + v);
         }
     }
     __syncthreads();
-    const int next = token_s != 0x7fffffff ? token_s : last_s;
+    const int next = token_s != 0x7fffffff ? token_s : tail_s;
     if (tid <= a.T)
         a.tokens[(size_t)b * (a.T + 1) + tid] = tid < k ? a.draft[(size_t)b * a.T + tid] : tid == k ? next : -1;
 }
 
 }  // namespace
 
-size_t verify_scratch_bytes(int B, int V) { return (size_t)B * slices_of(V) * sizeof(double2); }
+size_t verify_scratch_bytes(int B, int V) { return (size_t)B * slices_of(V) * sizeof(double); }
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
-    // CTAs for one wave (8 per SM); each warp takes slice after slice
+    // at most one wave of CTAs (8 per SM), every warp with as many slices as the others
     const int need = (slices_of(a.V) + kWarps - 1) / kWarps, wave = (148 * 8 + a.B - 1) / a.B;
-    const dim3 grid(need < wave ? need : wave, a.B);
+    const int rounds = (need + wave - 1) / wave;
+    const dim3 grid((need + rounds - 1) / rounds, a.B);
     const bool vec = a.V % 4 == 0 && (uintptr_t)a.target_probs % 16 == 0 && (uintptr_t)a.draft_probs % 16 == 0;
     if (vec) verify_sums_kernel<true><<<grid, 32 * kWarps, 0, s>>>(a);
     else verify_sums_kernel<false><<<grid, 32 * kWarps, 0, s>>>(a);

@@ -98,7 +98,7 @@ def test_workspace_queries():
     assert rda.rda_latent_decode_workspace_bytes(0, 1, 4, 512, 64) >= 256
     assert rda.rda_verify_drafts_workspace_bytes(2, 3, 0) == 0
     assert rda.rda_verify_drafts_workspace_bytes(2, 33, 10) == 0
-    assert rda.rda_verify_drafts_workspace_bytes(2, 3, 5000) >= 256 + 2 * 5 * 16
+    assert rda.rda_verify_drafts_workspace_bytes(2, 3, 5000) >= 256 + 2 * 5 * 8
 
 
 def test_binding_refuses_cpu_tensors():
