@@ -35,6 +35,7 @@ struct LatentArgs {
     float *lse;                  // forward: written (or null); backward: read
     int32_t *err;                // device error word
     uint64_t wait_ns;            // bound of every device-side wait
+    int debug_drop;              // fault injection (tests only): tiles from this one on are never filled; -1 = off
     // backward only
     const void *d_out;
     void *dq, *dq_shared, *dk, *dk_shared, *dv;
@@ -54,6 +55,7 @@ struct LatentDecodeArgs {
     float *lse;
     int32_t *err;
     uint64_t wait_ns;
+    int debug_drop;              // as above
     float *part;                 // workspace: partial outputs and their log-sum-exps
 };
 

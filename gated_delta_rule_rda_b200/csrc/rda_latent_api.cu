@@ -74,7 +74,9 @@ rda_status_t rda_latent_prefill(const void *q, const void *q_shared, const void 
     a.H = H; a.Dk = Dk; a.Ds = Ds; a.Dv = Dv; a.scale = scale; a.causal = causal != 0; a.dtype = dtype;
     a.out = out; a.lse = lse;
     a.err = static_cast<int32_t *>(workspace);
-    a.wait_ns = wait_settings().wait_ns;
+    const WaitSettings ws = wait_settings();
+    a.wait_ns = ws.wait_ns;
+    a.debug_drop = ws.drop_chunk;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return done(dtype == RDA_BF16 ? launch_latent_forward_tc(a, s) : launch_latent_forward_f32(a, s));
 }
@@ -112,7 +114,9 @@ rda_status_t rda_latent_backward(const void *q, const void *q_shared, const void
     a.out = const_cast<void *>(out); a.lse = const_cast<float *>(lse); a.d_out = d_out;
     a.dq = dq; a.dq_shared = dq_shared; a.dk = dk; a.dk_shared = dk_shared; a.dv = dv;
     a.err = static_cast<int32_t *>(workspace);
-    a.wait_ns = wait_settings().wait_ns;
+    const WaitSettings ws = wait_settings();
+    a.wait_ns = ws.wait_ns;
+    a.debug_drop = ws.drop_chunk;
     uint8_t *scratch = static_cast<uint8_t *>(workspace) + kErrorWordBytes;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == RDA_BF16) return done(launch_latent_backward_tc(a, scratch, s));
@@ -160,7 +164,9 @@ rda_status_t rda_latent_decode(const void *q, const void *q_shared, const void *
     a.B = B; a.T = T; a.H = H; a.Dl = Dl; a.Ds = Ds; a.scale = scale; a.dtype = dtype;
     a.out = out; a.lse = lse;
     a.err = static_cast<int32_t *>(workspace);
-    a.wait_ns = wait_settings().wait_ns;
+    const WaitSettings ws = wait_settings();
+    a.wait_ns = ws.wait_ns;
+    a.debug_drop = ws.drop_chunk;
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kErrorWordBytes);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return done(dtype == RDA_BF16 ? launch_latent_decode_tc(a, s) : launch_latent_decode_f32(a, s));

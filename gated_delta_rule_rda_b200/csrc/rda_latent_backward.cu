@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             RingPos p;
             int loaded = 0;
             for (; loaded < steps; ++loaded) {
+                if (loaded == a.debug_drop) break;
                 const int row = (first + loaded) * kRows;
                 if (loaded >= kStagesA && !w.wait(&B.q_empty[p.slot], p.phase ^ 1)) break;
                 uint8_t *dst = st_s + p.slot * stage;
@@ -462,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             RingPos pk, pv;
             int loaded_k = 0, loaded_v = 0;
             for (int i = 0; i < steps; ++i) {
+                if (i == a.debug_drop) break;
                 const int row = sk.start + (i < ahead ? i : i - ahead) * kKeys;
                 if (i >= kStK && !w.wait(&B.k_empty[pk.slot], pk.phase ^ 1)) break;
                 mbar_arrive_expect_tx(&B.k_full[pk.slot], nk * kMid);

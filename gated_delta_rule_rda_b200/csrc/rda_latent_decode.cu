@@ -580,6 +580,10 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
             Walk after = walk;
             const bool another = after.next(a);
             for (int t = walk.t0; t < walk.t1; ++t, ++it) {
+                if (it == (uint32_t)a.debug_drop) {
+                    more = false;
+                    break;
+                }
                 const int j = t * kTok + 16 * mine, page = page_next;
                 const bool ok = page >= 0 && page < a.num_pages;
                 if (t + 1 < walk.t1) page_next = page_of(walk, t + 1);
@@ -631,7 +635,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
                 }
             }
             walk = after;
-            more = another;
+            more = more && another;
         }
         cp_async_wait_all();                                // nothing lands after the CTA has left
     } else if (warp == kSoftWarp + softmax_warps(NT)) {

@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
             bool go = true;
             int loaded_k = 0, loaded_v = 0;
             for (int j = 0; j < nt; ++j) {
+                if (j == a.debug_drop) break;
                 const int row = sk.start + j * kBN;
                 if (j >= kStages) go = go && w.wait(&B.k_empty[p.slot], p.phase ^ 1);
                 if (!go) break;

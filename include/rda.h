@@ -428,6 +428,7 @@ rda_status_t rda_prefill_chunked_noalloc(const void *q, const void *k, const voi
  *                  behind the last sequence are neither read into a result nor written
  *   lse            device fp32 [total_q,H] or NULL
  *   Dk, Dv in {64, 128}, Ds in {0, 64}, H <= 1024; total * H * (Dk + Ds) < 2^31
+ * A device-side wait that runs out records RDA_ERR_TIMEOUT as in the prefill calls.
  * Preconditions, not checked: finite inputs within the sequences.  Sums, softmax
  * statistics and (for fp32) products are fp32; bf16 inputs run on the tensor cores,
  * with the probabilities rounded to bf16 for their product with v.
@@ -533,7 +534,9 @@ rda_status_t rda_verify_drafts(const int32_t *draft_tokens, const float *draft_p
  * in flight and returns, leaving the outputs from that chunk on and the final
  * state unwritten.  The context stays usable.  rda_debug_set_wait_fault(-1, 0)
  * turns it off (the default).  Not for production use: no other argument is
- * checked, and calls on other threads see the setting too.
+ * checked, and calls on other threads see the setting too.  The latent-attention
+ * calls on bf16 inputs follow it as well: from tile `drop_chunk` of a CTA on, its
+ * operands are never filled.
  */
 void rda_debug_set_wait_fault(int drop_chunk, unsigned long long wait_limit_ns);
 
