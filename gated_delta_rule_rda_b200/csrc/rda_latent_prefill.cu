@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
             };
             auto values = [&](int q, int j) {
                 ok = w.wait(&B.p_ready[q], j & 1) && ok;
-                ok = w.wait(&B.v_full[j % kStages], (j / kStages) & 1) && ok;
+                if (q == 0 || j >= n0) ok = w.wait(&B.v_full[j % kStages], (j / kStages) & 1) && ok;      // the first to use it
                 tc_fence_after();
                 if (ok) {
                     const uint64_t db = dv + (j % kStages) * nv * (kKChunk / 16);
