@@ -13,10 +13,10 @@
 //           then dV += P^T dO and dK += dS^T Q with P^T, dS^T as TMEM operands
 //   rows    128 query rows x 80 keys a step:  S = Q K^T,  dP = dO V^T,  then dQ += dS K
 //
-// In both, one thread issues the MMAs: the next step's scores go out before this
-// step's P is consumed, so that the tensor pipe and the eight element-wise warps
-// (a lane per key, or per query row; two warps share the columns of a lane)
-// work at the same time.  P and dS are rounded to bf16 for their products; p,
+// In both, one thread issues the first two products and another those that P and
+// dS go into, each as soon as its own operands are there, so that the tensor pipe
+// and the eight element-wise warps (a lane per key, or per query row; two warps
+// share the columns of a lane) work at the same time.  P and dS are rounded to bf16 for their products; p,
 // dp, delta and all sums are fp32.
 //
 // The key part that all heads share gets its gradient from every head: the
@@ -33,7 +33,8 @@ namespace {
 using namespace ptx;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 64 + 256;
+constexpr int kElemWarp = 2;                    // first element-wise warp
+constexpr int kThreads = 32 * (kElemWarp + 8 + 1);
 constexpr uint32_t kCols = 512;
 constexpr int kStat = 64;                       // query rows of a block of statistics
 constexpr uint32_t kBig = 128 * 128;            // 128 rows x 64 columns
@@ -224,38 +225,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMAs
+        // ------------------------------------------------------------ MMAs of S^T and dP^T
         if (elect_one() && steps > 0) {
-            const uint32_t idN64 = idesc_bf16(128, kRows, 0, 0), idV = idesc_bf16(128, a.Dv, 0, 1),
-                           idK = idesc_bf16(128, 64 * nk, 0, 1);
+            const uint32_t id = idesc_bf16(128, kRows, 0, 0);
             const uint64_t dk = smem_desc(smem_u32(k_s), 16, 1024, kSw128), dv = smem_desc(smem_u32(v_s), 16, 1024, kSw128);
             const uint64_t ds = smem_desc(smem_u32(st_s), 16, 1024, kSw128);          // K-major
-            const uint64_t dm = smem_desc(smem_u32(st_s), kSmall, 1024, kSw128);      // MN-major
             bool ok = w.wait(&B.kv_full, 0);
-            // S^T or dP^T of step i: `chunks` of 64 columns of the stationary tile against the stage's
+            // `chunks` of 64 columns of the stationary tile against the stage's
             auto product = [&](uint32_t d, uint64_t da, uint64_t db, int chunks) {
                 for (int c = 0; c < chunks; ++c)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(d, da + c * (kBig / 16) + 2 * k, db + c * (kSmall / 16) + 2 * k, idN64, c > 0 || k > 0);
+                        mma_bf16(d, da + c * (kBig / 16) + 2 * k, db + c * (kSmall / 16) + 2 * k, id, c > 0 || k > 0);
             };
-            RingPos next, now;
-            ok = w.wait(&B.q_full[0], 0) && ok;
-            tc_fence_after();
-            if (ok) product(tmem + kTS, dk, ds, nk);
-            mma_commit(&B.s_ready);
-            if (ok) product(tmem + kTdP, dv, ds + nk * (kSmall / 16), nv);
-            mma_commit(&B.dp_ready);
-            next.next(kStagesA);
+            RingPos p;
             for (int i = 0; i < steps; ++i) {
-                const uint64_t off = now.slot * (stage / 16), off_n = next.slot * (stage / 16);
-                if (i + 1 < steps) {
-                    ok = w.wait(&B.q_full[next.slot], next.phase) && ok;
-                    ok = w.wait(&B.s_free, i & 1) && ok;
-                    tc_fence_after();
-                    if (ok) product(tmem + kTS, dk, ds + off_n, nk);
-                    mma_commit(&B.s_ready);
-                }
+                const uint64_t off = p.slot * (stage / 16);
+                ok = w.wait(&B.q_full[p.slot], p.phase) && ok;
+                if (i > 0) ok = w.wait(&B.s_free, (i - 1) & 1) && ok;
+                tc_fence_after();
+                if (ok) product(tmem + kTS, dk, ds + off, nk);
+                mma_commit(&B.s_ready);
+                if (i > 0) ok = w.wait(&B.dp_free, (i - 1) & 1) && ok;
+                tc_fence_after();
+                if (ok) product(tmem + kTdP, dv, ds + off + nk * (kSmall / 16), nv);
+                mma_commit(&B.dp_ready);
+                p.next(kStagesA);
+            }
+            // everything issued has completed with the last commit
+            if (B.abort) w.drain(&B.dp_ready, (steps - 1) & 1, Waiter::now());
+        }
+        __syncwarp();
+    } else if (warp == kElemWarp + 8) {
+        // ------------------------------------------------------------ MMAs of dV and dK
+        if (elect_one() && steps > 0) {
+            const uint32_t idV = idesc_bf16(128, a.Dv, 0, 1), idK = idesc_bf16(128, 64 * nk, 0, 1);
+            const uint64_t dm = smem_desc(smem_u32(st_s), kSmall, 1024, kSw128);      // MN-major
+            bool ok = true;
+            RingPos p;
+            for (int i = 0; i < steps; ++i) {
+                const uint64_t off = p.slot * (stage / 16);
                 ok = w.wait(&B.p_ready, i & 1) && ok;
                 tc_fence_after();
                 if (ok) {
@@ -264,12 +273,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_bf16_ta(tmem + kTdV, tmem + kTP + 8 * k, dm + off + nk * (kSmall / 16) + 128 * k, idV, i > 0 || k > 0);
                 }
                 mma_commit(&B.dv_done);
-                if (i + 1 < steps) {
-                    ok = w.wait(&B.dp_free, i & 1) && ok;
-                    tc_fence_after();
-                    if (ok) product(tmem + kTdP, dv, ds + off_n + nk * (kSmall / 16), nv);
-                    mma_commit(&B.dp_ready);
-                }
                 ok = w.wait(&B.ds_ready, i & 1) && ok;
                 tc_fence_after();
                 if (ok) {
@@ -277,10 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; ++k)
                         mma_bf16_ta(tmem + kTdK, tmem + kTdS + 8 * k, dm + off + 128 * k, idK, i > 0 || k > 0);
                 }
-                mma_commit(&B.q_empty[now.slot]);
+                mma_commit(&B.q_empty[p.slot]);
                 mma_commit(&B.dk_done);
-                now.next(kStagesA);
-                next.next(kStagesA);
+                p.next(kStagesA);
             }
             if (B.abort) w.drain(&B.dk_done, (steps - 1) & 1, Waiter::now());
         }
@@ -488,47 +490,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMAs
+        // ------------------------------------------------------------ MMAs of S and dP
         if (elect_one() && steps > 0) {
-            const uint32_t idN = idesc_bf16(128, kKeys, 0, 0), idQ = idesc_bf16(128, 64 * nk, 0, 1);
+            const uint32_t id = idesc_bf16(128, kKeys, 0, 0);
             const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024, kSw128), dO = smem_desc(smem_u32(o_s), 16, 1024, kSw128);
             const uint64_t dk = smem_desc(smem_u32(k_s), 16, 1024, kSw128), dv = smem_desc(smem_u32(v_s), 16, 1024, kSw128);
-            const uint64_t dm = smem_desc(smem_u32(k_s), kMid, 1024, kSw128);        // K, MN-major
             bool ok = w.wait(&B.q_full, 0);
             auto product = [&](uint32_t d, uint64_t da, uint64_t db, int chunks) {
                 for (int c = 0; c < chunks; ++c)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(d, da + c * (kBig / 16) + 2 * k, db + c * (kMid / 16) + 2 * k, idN, c > 0 || k > 0);
+                        mma_bf16(d, da + c * (kBig / 16) + 2 * k, db + c * (kMid / 16) + 2 * k, id, c > 0 || k > 0);
             };
-            RingPos next, now, vs;
-            for (int i = -1; i < steps; ++i) {
-                if (i + 1 < steps) {
-                    ok = w.wait(&B.k_full[next.slot], next.phase) && ok;
-                    if (i >= 0) ok = w.wait(&B.s_free, i & 1) && ok;
-                    tc_fence_after();
-                    if (ok) product(tmem + kUS, dq, dk + next.slot * nk * (kMid / 16), nk);
-                    mma_commit(&B.s_ready);
-                    next.next(kStK);
-                    ok = w.wait(&B.v_full[vs.slot], vs.phase) && ok;
-                    if (i >= 0) ok = w.wait(&B.dp_free, i & 1) && ok;
-                    tc_fence_after();
-                    if (ok) product(tmem + kUdP, dO, dv + vs.slot * nv * (kMid / 16), nv);
-                    mma_commit(&B.dp_ready);
-                    mma_commit(&B.v_empty[vs.slot]);
-                    vs.next(kStV);
-                }
-                if (i < 0) continue;
+            RingPos ks, vs;
+            for (int i = 0; i < steps; ++i) {
+                ok = w.wait(&B.k_full[ks.slot], ks.phase) && ok;
+                if (i > 0) ok = w.wait(&B.s_free, (i - 1) & 1) && ok;
+                tc_fence_after();
+                if (ok) product(tmem + kUS, dq, dk + ks.slot * nk * (kMid / 16), nk);
+                mma_commit(&B.s_ready);
+                ks.next(kStK);
+                ok = w.wait(&B.v_full[vs.slot], vs.phase) && ok;
+                if (i > 0) ok = w.wait(&B.dp_free, (i - 1) & 1) && ok;
+                tc_fence_after();
+                if (ok) product(tmem + kUdP, dO, dv + vs.slot * nv * (kMid / 16), nv);
+                mma_commit(&B.v_empty[vs.slot]);
+                mma_commit(&B.dp_ready);
+                vs.next(kStV);
+            }
+            // everything issued has completed with the last commit
+            if (B.abort) w.drain(&B.dp_ready, (steps - 1) & 1, Waiter::now());
+        }
+        __syncwarp();
+    } else if (warp == kElemWarp + 8) {
+        // ------------------------------------------------------------ MMAs of dQ
+        if (elect_one() && steps > 0) {
+            const uint32_t id = idesc_bf16(128, 64 * nk, 0, 1);
+            const uint64_t dm = smem_desc(smem_u32(k_s), kMid, 1024, kSw128);         // K, MN-major
+            bool ok = true;
+            RingPos p;
+            for (int i = 0; i < steps; ++i) {
                 ok = w.wait(&B.ds_ready, i & 1) && ok;
                 tc_fence_after();
                 if (ok && i >= ahead) {
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        mma_bf16_ta(tmem + kUdQ, tmem + kUdS + 8 * k, dm + now.slot * nk * (kMid / 16) + 128 * k, idQ, i > ahead || k > 0);
+                        mma_bf16_ta(tmem + kUdQ, tmem + kUdS + 8 * k, dm + p.slot * nk * (kMid / 16) + 128 * k, id, i > ahead || k > 0);
                 }
-                mma_commit(&B.k_empty[now.slot]);
+                mma_commit(&B.k_empty[p.slot]);
                 mma_commit(&B.dq_done);
-                now.next(kStK);
+                p.next(kStK);
             }
             if (B.abort) w.drain(&B.dq_done, (steps - 1) & 1, Waiter::now());
         }

@@ -19,8 +19,8 @@
 // of 64 costs 48 against 32.
 //
 //   warp 0       producer: Q, then K and V tiles by TMA (two stages each)
-//   warp 1       one thread issues the MMAs: for each tile the next scores, then
-//                this P's product
+//   warp 1       one thread issues the scores' MMAs, one of warp 10 those of P: each
+//                waits for its own operands only, and neither for the other's
 //   warps 2..9   softmax: one thread per query row (no shuffles); O is rescaled
 //                only when a row's maximum has grown by more than 2^8
 //
@@ -40,7 +40,8 @@ using namespace ptx;
 constexpr int kBM = 128, kQ = 2;             // rows of a query tile, tiles of a CTA
 constexpr int kBN = 80;                      // keys of a tile
 constexpr int kStages = 2;
-constexpr int kThreads = 64 + 128 * kQ;
+constexpr int kSoftWarp = 2;                 // first softmax warp
+constexpr int kThreads = 32 * (kSoftWarp + 4 * kQ + 1);
 constexpr uint32_t kQChunk = kBM * 128, kKChunk = kBN * 128;      // 64 columns of a tile
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kTO = 0, kTS = 256, kTP = kTS + 2 * kBN;       // TMEM columns: O (128 each), S (80), P (40)
@@ -164,51 +165,57 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMAs
+        // ------------------------------------------------------------ MMAs of the scores
         if (elect_one() && nt > 0) {
-            const uint32_t idS = idesc_bf16(kBM, kBN, 0, 0), idO = idesc_bf16(kBM, a.Dv, 0, 1);
+            const uint32_t idS = idesc_bf16(kBM, kBN, 0, 0);
             const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024, kSw128), dk = smem_desc(smem_u32(k_s), 16, 1024, kSw128);
-            const uint64_t dv = smem_desc(smem_u32(v_s), kKChunk, 1024, kSw128);
             bool ok = true;
-            auto scores = [&](int q, int j) {
-                ok = (j > 0 ? w.wait(&B.s_free[q], (j - 1) & 1) : w.wait(&B.q_full[q], 0)) && ok;
-                tc_fence_after();
-                if (ok)
-                    for (int c = 0; c < nk; ++c) {
-                        const uint64_t da = dq + (q * nk + c) * (kQChunk / 16), db = dk + ((j % kStages) * nk + c) * (kKChunk / 16);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + kTS + q * kBN, da + 2 * k, db + 2 * k, idS, c > 0 || k > 0);
-                    }
-                mma_commit(&B.s_ready[q]);
-            };
-            auto values = [&](int q, int j) {
-                ok = w.wait(&B.p_ready[q], j & 1) && ok;
-                if (q == 0 || j >= n0) ok = w.wait(&B.v_full[j % kStages], (j / kStages) & 1) && ok;      // the first to use it
-                tc_fence_after();
-                if (ok) {
-                    const uint64_t db = dv + (j % kStages) * nv * (kKChunk / 16);
-#pragma unroll
-                    for (int k = 0; k < kBN / 16; ++k)
-                        mma_bf16_ta(tmem + kTO + q * 128, tmem + kTP + q * (kBN / 2) + 8 * k, db + 128 * k, idO, j > 0 || k > 0);
-                }
-                mma_commit(&B.pv_done[q]);
-            };
-            ok = w.wait(&B.k_full[0], 0) && ok;
-            if (n0 > 0) scores(0, 0);
-            if (n1 > 0) scores(1, 0);
-            mma_commit(&B.k_empty[0]);
+            RingPos ks;
             for (int j = 0; j < nt; ++j) {
-                const int x = j + 1;
-                if (x < nt) ok = w.wait(&B.k_full[x % kStages], (x / kStages) & 1) && ok;
-                if (x < n0) scores(0, x);
-                if (j < n0) values(0, j);
-                if (x < n1) scores(1, x);
-                if (x < nt) mma_commit(&B.k_empty[x % kStages]);
-                if (j < n1) values(1, j);
-                mma_commit(&B.v_empty[j % kStages]);
+                ok = w.wait(&B.k_full[ks.slot], ks.phase) && ok;
+                for (int q = 0; q < kQ; ++q) {
+                    if (j >= (q ? n1 : n0)) continue;
+                    ok = (j > 0 ? w.wait(&B.s_free[q], (j - 1) & 1) : w.wait(&B.q_full[q], 0)) && ok;
+                    tc_fence_after();
+                    if (ok)
+                        for (int c = 0; c < nk; ++c) {
+                            const uint64_t da = dq + (q * nk + c) * (kQChunk / 16), db = dk + (ks.slot * nk + c) * (kKChunk / 16);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) mma_bf16(tmem + kTS + q * kBN, da + 2 * k, db + 2 * k, idS, c > 0 || k > 0);
+                        }
+                    mma_commit(&B.s_ready[q]);
+                }
+                mma_commit(&B.k_empty[ks.slot]);
+                ks.next(kStages);
             }
             // everything issued has completed with the last commit
+            if (B.abort) w.drain(&B.k_empty[(nt - 1) % kStages], ((nt - 1) / kStages) & 1, Waiter::now());
+        }
+        __syncwarp();
+    } else if (warp == kSoftWarp + 8) {
+        // ------------------------------------------------------------ MMAs of the values
+        if (elect_one() && nt > 0) {
+            const uint32_t idO = idesc_bf16(kBM, a.Dv, 0, 1);
+            const uint64_t dv = smem_desc(smem_u32(v_s), kKChunk, 1024, kSw128);
+            bool ok = true;
+            RingPos vs;
+            for (int j = 0; j < nt; ++j) {
+                ok = w.wait(&B.v_full[vs.slot], vs.phase) && ok;
+                for (int q = 0; q < kQ; ++q) {
+                    if (j >= (q ? n1 : n0)) continue;
+                    ok = w.wait(&B.p_ready[q], j & 1) && ok;
+                    tc_fence_after();
+                    if (ok) {
+                        const uint64_t db = dv + vs.slot * nv * (kKChunk / 16);
+#pragma unroll
+                        for (int k = 0; k < kBN / 16; ++k)
+                            mma_bf16_ta(tmem + kTO + q * 128, tmem + kTP + q * (kBN / 2) + 8 * k, db + 128 * k, idO, j > 0 || k > 0);
+                    }
+                    mma_commit(&B.pv_done[q]);
+                }
+                mma_commit(&B.v_empty[vs.slot]);
+                vs.next(kStages);
+            }
             if (B.abort) w.drain(&B.v_empty[(nt - 1) % kStages], ((nt - 1) / kStages) & 1, Waiter::now());
         }
         __syncwarp();
