@@ -105,33 +105,6 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, uint32_t tile_bytes, in
             *reinterpret_cast<uint4 *>(tile + c * tile_bytes + sw128(from + (e >> 3), e & 7)) = make_uint4(0, 0, 0, 0);
 }
 
-// NC columns of a row of an accumulator (my lane), times f, as bf16 or fp32 to `out`.
-template <typename T>
-__device__ __forceinline__ void store_cols(uint32_t t, int cols, float f, T *out, bool mine, bool zero) {
-#pragma unroll 1
-    for (int c = 0; c < cols; c += 32) {
-        float x[32];
-        if (zero) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = 0.f;
-        } else {
-            tmem_ld32(t + c, x);
-            tmem_wait_ld();
-        }
-        if (!mine) continue;
-        if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4 *>(out + c + i) = make_uint4(pack2(x[i] * f, x[i + 1] * f), pack2(x[i + 2] * f, x[i + 3] * f),
-                                                                     pack2(x[i + 4] * f, x[i + 5] * f), pack2(x[i + 6] * f, x[i + 7] * f));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4 *>(out + c + i) = make_float4(x[i] * f, x[i + 1] * f, x[i + 2] * f, x[i + 3] * f);
-        }
-    }
-}
-
 // ---------------------------------------------------------------------------
 // dK and dV: one CTA per (128 keys, head).
 // ---------------------------------------------------------------------------
@@ -368,14 +341,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.wait(&B.dk_done, (steps - 1) & 1);
             tc_fence_after();
         }
-        const bool mine = key < sk.len;
-        const size_t at = (size_t)(sk.start + key) * a.H + h;
-        if (half == 0) {
-            store_cols(tmem + kTdV + lanes, a.Dv, 1.f, static_cast<__nv_bfloat16 *>(a.dv) + at * a.Dv, mine, steps == 0);
-        } else {
-            store_cols(tmem + kTdK + lanes, a.Dk, a.scale, static_cast<__nv_bfloat16 *>(a.dk) + at * a.Dk, mine, steps == 0);
-            if (a.Ds)
-                store_cols(tmem + kTdK + a.Dk + lanes, a.Ds, a.scale, a.dks_heads + at * a.Ds, mine, steps == 0);
+        // through the stages, which no product reads any more
+        const int rows = sk.len - k0 - 32 * quad;
+        const bool any = steps > 0;
+        uint8_t *buf = st_s + (warp - kElemWarp) * 4096;
+        const size_t at = (size_t)(sk.start + k0 + 32 * quad) * a.H + h;
+        uint4 x[8];
+#pragma unroll 1
+        for (int c = 0; c < (half ? nd : nv); ++c) {
+            const int D = half ? a.Dk : a.Dv;
+            tmem_row_bf16(tmem + (half ? kTdK : kTdV) + 64 * c + lanes, half ? a.scale : 1.f, any, x);
+            store_rows_128(buf, x, static_cast<__nv_bfloat16 *>(half ? a.dk : a.dv) + at * D + 64 * c, (size_t)a.H * D * 2, rows);
+        }
+        if (a.Ds) {
+            // the shared part: 32 of its 64 columns each
+            tmem_row_f32(tmem + kTdK + a.Dk + 32 * half + lanes, a.scale, any, x);
+            store_rows_128(buf, x, a.dks_heads + at * a.Ds + 32 * half, (size_t)a.H * a.Ds * 4, rows);
         }
     }
     tc_fence_before();
@@ -624,14 +605,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.wait(&B.dq_done, (steps - 1) & 1);
             tc_fence_after();
         }
-        const size_t at = (size_t)(sq.start + row) * a.H + h;
-        const bool mine = r < rows;
-        // the columns in halves: Dk / 2 and Ds / 2 each
-        store_cols(tmem + kUdQ + half * (a.Dk / 2) + lanes, a.Dk / 2, a.scale,
-                   static_cast<__nv_bfloat16 *>(a.dq) + at * a.Dk + half * (a.Dk / 2), mine, steps == 0);
-        if (a.Ds)
-            store_cols(tmem + kUdQ + a.Dk + half * (a.Ds / 2) + lanes, a.Ds / 2, a.scale,
-                       static_cast<__nv_bfloat16 *>(a.dq_shared) + at * a.Ds + half * (a.Ds / 2), mine, steps == 0);
+        // through the stages, which no product reads any more; chunks of 64 columns in turn
+        uint8_t *buf = k_s + (warp - kElemWarp) * 4096;
+        const size_t at = (size_t)(sq.start + r0 + 32 * quad) * a.H + h;
+#pragma unroll 1
+        for (int c = half; c < nk; c += 2) {
+            uint4 x[8];
+            tmem_row_bf16(tmem + kUdQ + 64 * c + lanes, a.scale, steps > 0, x);
+            if (c < nd)
+                store_rows_128(buf, x, static_cast<__nv_bfloat16 *>(a.dq) + at * a.Dk + 64 * c, (size_t)a.H * a.Dk * 2, rows - 32 * quad);
+            else
+                store_rows_128(buf, x, static_cast<__nv_bfloat16 *>(a.dq_shared) + at * a.Ds, (size_t)a.H * a.Ds * 2, rows - 32 * quad);
+        }
     }
     tc_fence_before();
     __syncthreads();

@@ -322,27 +322,16 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
             w.wait(&B.pv_done[q], (tiles - 1) & 1);
             tc_fence_after();
         }
-        const size_t at = (size_t)(sq.start + row) * a.H + h;
-        const bool mine = r < rows;
         const float f = l > 0.f ? 1.f / l : 0.f;
-        if (mine && a.lse) a.lse[at] = l > 0.f ? (m * sc + lg2(l)) * kLn2 : -INFINITY;
-        uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * a.Dv);
+        if (r < rows && a.lse) a.lse[(size_t)(sq.start + row) * a.H + h] = l > 0.f ? (m * sc + lg2(l)) * kLn2 : -INFINITY;
+        // through the tile's own query rows, which no product reads any more
+        uint8_t *buf = q_s + q * nk * kQChunk + quad * 4096;
+        auto *out = static_cast<__nv_bfloat16 *>(a.out) + ((size_t)(sq.start + r0 + q * kBM + 32 * quad) * a.H + h) * a.Dv;
 #pragma unroll 1
-        for (int c = 0; c < a.Dv; c += 32) {
-            float o[32];
-            if (tiles > 0) {
-                tmem_ld32(t_o + c, o);
-                tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            }
-            if (mine) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 8)
-                    out[(c + i) / 8] = make_uint4(pack2(o[i] * f, o[i + 1] * f), pack2(o[i + 2] * f, o[i + 3] * f),
-                                                  pack2(o[i + 4] * f, o[i + 5] * f), pack2(o[i + 6] * f, o[i + 7] * f));
-            }
+        for (int c = 0; c < nv; ++c) {
+            uint4 x[8];
+            tmem_row_bf16(t_o + 64 * c, f, tiles > 0, x);
+            store_rows_128(buf, x, out + 64 * c, (size_t)a.H * a.Dv * 2, rows - 32 * quad);
         }
     }
     tc_fence_before();

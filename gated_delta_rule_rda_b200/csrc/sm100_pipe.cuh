@@ -201,6 +201,54 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // Byte offset of 16-byte chunk `c` (0..7) of row `row` in a tile of 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t c) { return row * 128 + ((c ^ (row & 7)) << 4); }
 
+// 128 bytes of each of a warp's 32 rows (lane = row) to global memory, rows `stride` bytes apart, the first `rows`
+// of them.  Through 4 KiB of shared memory, so that a store covers four whole rows: straight from the lanes each
+// store touches 32 lines (9,700 cycles for 128 rows of 384 columns, 3,000 this way).
+__device__ __forceinline__ void store_rows_128(uint8_t *buf, const uint4 (&x)[8], void *out, size_t stride, int rows) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(buf + sw128(lane, c)) = x[c];
+    __syncwarp();
+    uint8_t *to = static_cast<uint8_t *>(out) + (lane >> 3) * stride + (lane & 7) * 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i, to += 4 * stride) {
+        const int r = 4 * i + (lane >> 3);
+        if (r < rows) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(buf + sw128(r, lane & 7));
+    }
+    __syncwarp();
+}
+// 64 columns of an accumulator times f, as bf16 (zeros where there is no accumulator).
+__device__ __forceinline__ void tmem_row_bf16(uint32_t t, float f, bool any, uint4 (&x)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float v[32];
+        if (any) {
+            tmem_ld32(t + 32 * h, v);
+            tmem_wait_ld();
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = any ? v[i] * f : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[4 * h + i] = make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
+                                      pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
+    }
+}
+// 32 columns times f, as fp32.
+__device__ __forceinline__ void tmem_row_f32(uint32_t t, float f, bool any, uint4 (&x)[8]) {
+    float v[32];
+    if (any) {
+        tmem_ld32(t, v);
+        tmem_wait_ld();
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = any ? v[i] * f : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                          __float_as_uint(v[4 * i + 3]));
+}
+
 // The dynamic shared memory rounded up to 1024 bytes, as shared memory.
 __device__ __forceinline__ uint8_t *align_1024(uint8_t *raw) { return raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u); }
 
