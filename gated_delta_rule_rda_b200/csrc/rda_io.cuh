@@ -48,9 +48,13 @@ template <> struct Io<__nv_bfloat16> {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// The same for rows that are read once and whole: the line's neighbour is brought to L2 as well.
+__device__ __forceinline__ void cp_async16_row(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // `bytes` (16 or 0) come from src, the rest of the 16 are zeros.
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // Arrives on an mbarrier (shared address) once this thread's copies so far have landed; the barrier's count
 // includes the arrival.

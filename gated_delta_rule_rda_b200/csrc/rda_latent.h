@@ -36,6 +36,7 @@ struct LatentArgs {
     int32_t *err;                // device error word
     uint64_t wait_ns;            // bound of every device-side wait
     int debug_drop;              // fault injection (tests only): tiles from this one on are never filled; -1 = off
+    const int2 *order;           // tiles by work (TileOrder), or null: by their places
     // backward only
     const void *d_out;
     void *dq, *dq_shared, *dk, *dk_shared, *dv;
@@ -97,7 +98,16 @@ __device__ __forceinline__ int find_tile(const int32_t *cu, int num_seqs, int to
     *t = slot - (clamped(cu, lo, total) / tile + lo);
     return lo;
 }
-inline int tile_slots(int total, int num_seqs, int tile) { return total / tile + num_seqs; }
+__host__ __device__ inline int tile_slots(int total, int num_seqs, int tile) { return total / tile + num_seqs; }
+
+// The tiles of a packed batch in the order of their work, most first, so that
+// the last CTAs are short.  Tiles are of query rows (work: units of keys that they
+// see) or of keys (units of query rows that see them).
+struct TileOrder {
+    int keys, tile, unit;
+    int2 *out;                   // [slots]: {sequence, tile}, then {-1, -1}
+};
+size_t order_bytes(int total, int num_seqs, int tile);
 
 cudaError_t launch_latent_forward_f32(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_latent_backward_f32(const LatentArgs &a, cudaStream_t s);
@@ -108,7 +118,8 @@ cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s);
 // bf16: tensor cores
 cudaError_t launch_latent_backward_tc(const LatentArgs &a, void *scratch, cudaStream_t s);
 size_t latent_backward_tc_scratch_bytes(int total_q, int total_k, int num_seqs, int H, int Ds);
-cudaError_t launch_latent_forward_tc(const LatentArgs &a, cudaStream_t s);
+cudaError_t launch_latent_forward_tc(const LatentArgs &a, void *scratch, cudaStream_t s);
+size_t latent_prefill_scratch_bytes(int total_q, int num_seqs);
 cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s);
 

@@ -25,6 +25,7 @@
 #include <cstring>
 
 #include "rda_latent.h"
+#include "rda_latent_order.cuh"
 #include "sm100_pipe.cuh"
 
 namespace rda {
@@ -57,39 +58,51 @@ struct Maps {
 // delta, [head][block][2][64].  Rows behind the sequence's end, and rows that
 // saw no key, get +inf: their p is 2^-inf = 0.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) latent_stats_kernel(const LatentArgs a, float *stats) {
+// Two more CTAs (of the row behind the heads) put the tiles of the other kernels in order.
+__global__ void __launch_bounds__(256) latent_stats_kernel(const LatentArgs a, float *stats, const TileOrder rows,
+                                                           const TileOrder keys) {
+    if (blockIdx.y == a.H) {
+        if (blockIdx.x < 2) order_tiles(a, blockIdx.x ? keys : rows);
+        return;
+    }
     int t;
     const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, kStat, blockIdx.x, &t);
     const SeqSpan sq = seq_span(a.cu_q, n, a.total_q);
-    const int h = blockIdx.y, r = threadIdx.x >> 2, part = threadIdx.x & 3, row = t * kStat + r;
-    float x = 0.f;
-    const size_t at = (size_t)(sq.start + row) * a.H + h;
-    if (row < sq.len) {
-        const uint4 *o = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.out) + at * a.Dv);
-        const uint4 *d = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.d_out) + at * a.Dv);
-        uint4 u[4], v[4];
+    const int h = blockIdx.y;
+    // a lane per 16 bytes of a row: 16 or 8 lanes a row, all loads of a warp's 8 rows in flight at once
+    const int lanes = a.Dv / 8, per = 32 / lanes, lane = threadIdx.x & 31, part = lane % lanes;
+    const int first = (threadIdx.x >> 5) * 8 + lane / lanes;
+    uint4 u[4], v[4];
+    float lse[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (part + 4 * i < a.Dv / 8) u[i] = o[part + 4 * i], v[i] = d[part + 4 * i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (part + 4 * i < a.Dv / 8) {
-                const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&u[i]);
-                const __nv_bfloat162 *q = reinterpret_cast<const __nv_bfloat162 *>(&v[i]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = __bfloat1622float2(p[k]), g = __bfloat1622float2(q[k]);
-                    x = fmaf(f.x, g.x, fmaf(f.y, g.y, x));
-                }
-            }
+    for (int i = 0; i < 4; ++i) {
+        const int row = t * kStat + first + i * per;
+        u[i] = v[i] = make_uint4(0, 0, 0, 0);
+        lse[i] = -INFINITY;
+        if (i * per < 8 && row < sq.len) {
+            const size_t at = (size_t)(sq.start + row) * a.H + h;
+            u[i] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.out) + at * a.Dv)[part];
+            v[i] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.d_out) + at * a.Dv)[part];
+            lse[i] = a.lse[at];
+        }
     }
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    x += __shfl_xor_sync(0xffffffffu, x, 2);
-    if (part == 0) {
-        float *s = stats + ((size_t)h * gridDim.x + blockIdx.x) * 2 * kStat;
-        const float lse = row < sq.len ? a.lse[at] : -INFINITY;
-        s[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;
-        s[kStat + r] = row < sq.len ? x : 0.f;
+    float *s = stats + ((size_t)h * gridDim.x + blockIdx.x) * 2 * kStat;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i * per >= 8) break;
+        float x = 0.f;
+        const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&u[i]);
+        const __nv_bfloat162 *q = reinterpret_cast<const __nv_bfloat162 *>(&v[i]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = __bfloat1622float2(p[k]), g = __bfloat1622float2(q[k]);
+            x = fmaf(f.x, g.x, fmaf(f.y, g.y, x));
+        }
+        for (int off = lanes / 2; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        if (part == 0) {
+            s[first + i * per] = lse[i] == -INFINITY ? INFINITY : lse[i] * kLog2e;
+            s[kStat + first + i * per] = x;
+        }
     }
 }
 
@@ -128,10 +141,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Waiter w{&B.abort, a.err, a.wait_ns};
 
-    // heads side by side; the first keys of a sequence (which the most queries see) first
+    // heads side by side, tiles with the most work first
     const int h = blockIdx.x % a.H;
     int t;
-    const int n = find_tile(a.cu_k, a.num_seqs, a.total_k, 128, blockIdx.x / a.H, &t);
+    const int n = tile_at(a, true, 128, blockIdx.x / a.H, gridDim.x / a.H, &t);
+    if (n < 0) return;
     const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
     const int k0 = t * 128, more = sk.len - sq.len;
     if (k0 >= sk.len) return;
@@ -401,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int h = blockIdx.x % a.H;
     int t;
-    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, 128, (int)(gridDim.x / a.H - 1 - blockIdx.x / a.H), &t);
+    const int n = tile_at(a, false, 128, blockIdx.x / a.H, gridDim.x / a.H, &t);
+    if (n < 0) return;
     const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
     const int r0 = t * 128, more = sk.len - sq.len;
     const int rows = min(128, sq.len - r0);
@@ -642,8 +657,10 @@ bool make_maps(Maps *m, const LatentArgs &a, uint32_t box_q, uint32_t box_k) {
 
 }  // namespace
 
+// statistics, the shared key part's gradients by head, and the two orders
 size_t latent_backward_tc_scratch_bytes(int total_q, int total_k, int num_seqs, int H, int Ds) {
-    return stats_bytes(total_q, num_seqs, H) + (size_t)total_k * H * Ds * sizeof(float);
+    return stats_bytes(total_q, num_seqs, H) + (size_t)total_k * H * Ds * sizeof(float) + order_bytes(total_q, num_seqs, 128) +
+           order_bytes(total_k, num_seqs, 128);
 }
 
 cudaError_t launch_latent_backward_tc(const LatentArgs &a0, void *scratch, cudaStream_t s) {
@@ -654,19 +671,25 @@ cudaError_t launch_latent_backward_tc(const LatentArgs &a0, void *scratch, cudaS
     if (e == cudaSuccess) e = allow_smem<latent_dq_kernel>(232448);
     if (e != cudaSuccess) return e;
     const int blocks = tile_slots(a.total_q, a.num_seqs, kStat), nk = (a.Dk + a.Ds) / 64, nv = a.Dv / 64;
-    if (a.total_q > 0) {
-        latent_stats_kernel<<<dim3(blocks, a.H), 256, 0, s>>>(a, stats);
+    TileOrder rows{0, 128, kKeys, nullptr}, keys{1, 128, kRows, nullptr};
+    rows.out = reinterpret_cast<int2 *>(a.dks_heads + (size_t)a.total_k * a.H * a.Ds);
+    keys.out = rows.out + tile_slots(a.total_q, a.num_seqs, 128);
+    const bool sorted = a.num_seqs > 1;           // two CTAs beside the others (blocks >= num_seqs >= 2)
+    if (a.total_q > 0 || sorted) {
+        latent_stats_kernel<<<dim3(blocks, a.H + sorted), 256, 0, s>>>(a, stats, rows, keys);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     Maps m;
     // dQ first: it corrects the statistics that dK uses
     if (a.total_q > 0) {
         if (!make_maps(&m, a, 128, kKeys)) return cudaErrorInvalidValue;
+        a.order = sorted ? rows.out : nullptr;
         latent_dq_kernel<<<tile_slots(a.total_q, a.num_seqs, 128) * a.H, kThreads, smem_b(nk, nv), s>>>(m, a, stats, blocks);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (a.total_k > 0) {
         if (!make_maps(&m, a, kRows, 128)) return cudaErrorInvalidValue;
+        a.order = sorted ? keys.out : nullptr;
         latent_dkv_kernel<<<tile_slots(a.total_k, a.num_seqs, 128) * a.H, kThreads, smem_a(nk, nv), s>>>(m, a, stats, blocks);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }

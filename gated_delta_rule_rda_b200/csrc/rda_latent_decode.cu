@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
                         const uint32_t to = dst + (lane >> 3) * kBox + 16 * mine * 128;
                         if (have == 16) {
 #pragma unroll 8
-                            for (int r = 0; r < 16; ++r, x += D) cp_async16(to + sw128(r, lane & 7), x);
+                            for (int r = 0; r < 16; ++r, x += D) cp_async16_row(to + sw128(r, lane & 7), x);
                         } else {
 #pragma unroll 4
                             for (int r = 0; r < 16; ++r, x += r < have ? D : 0)

@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(256) latent_shared_sum_kernel(const float *par
     if (row >= rows || row >= cu_k[num_seqs]) return;
     const int c = (int)(e % Ds);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int h = 0; h < H; ++h) {
         const float4 y = *reinterpret_cast<const float4 *>(parts + ((size_t)row * H + h) * Ds + c);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
