@@ -45,12 +45,27 @@ __device__ __forceinline__ void load_rows(float *dst, int ld, const T *part, int
     }
 }
 
+// The same copied asynchronously (fp32).
+template <int ROWS, int NT>
+__device__ __forceinline__ void copy_rows(float *dst, int ld, const float *part, int D0, const float *shared, int D1, int Hs,
+                                          long row0, int n, int H, int h) {
+    const int r0 = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * 4;
+#pragma unroll
+    for (int r = r0; r < ROWS; r += NT / 16) {
+        const size_t row = (size_t)(row0 + min(r, n - 1));
+        for (int c = c0; c < D0 + D1; c += 64)
+            cp_async16_or_zero((uint32_t)__cvta_generic_to_shared(dst + r * ld + c),
+                               c < D0 ? part + (row * H + h) * D0 + c : shared + (row * Hs + (Hs == 1 ? 0 : h)) * D1 + (c - D0),
+                               r < n ? 16 : 0);
+    }
+}
+
 // acc[i][j] += a[RI ty + i] . b[tx + 16 j] over D
 template <int RI>
 __device__ __forceinline__ void dot(float (&acc)[RI][4], const float *a, int lda, const float *b, int ldb, int D) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const float *ar = a + RI * ty * lda, *br = b + tx * ldb;
-#pragma unroll 2
+#pragma unroll(RI == 1 ? 8 : 2)
     for (int d = 0; d < D; d += 4) {
         float4 x[RI], y[4];
 #pragma unroll
@@ -69,7 +84,7 @@ __device__ __forceinline__ void dot(float (&acc)[RI][4], const float *a, int lda
 template <int RI, int NC>
 __device__ __forceinline__ void rows_times(float (&acc)[RI][NC][4], const float *w, const float *b, int ldb) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll 1
+#pragma unroll(RI == 1 ? 4 : 1)
     for (int j = 0; j < kTile; j += 4) {
         float4 x[RI];
 #pragma unroll
@@ -140,14 +155,16 @@ __device__ __forceinline__ bool seen(const LatentArgs &a, int i, int j, int lq, 
 // Forward: one CTA per (RI NT / 16 query rows, head), online softmax over key
 // tiles.  RI = 4 with 512 threads (128 rows) reads each operand for four products
 // and keeps 16 warps on an SM; RI = 1 with 256 threads (16 rows) makes eight times
-// as many CTAs, for calls that would leave SMs empty.
+// as many CTAs, for calls that would leave SMs empty, and copies the next key tile
+// while it works on one.
 // ---------------------------------------------------------------------------
 template <typename T, int NDV, int RI, int NT>
 __global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a) {
     extern __shared__ __align__(16) float smem[];
     constexpr int M = RI * NT / 16;
     const int D = a.Dk + a.Ds, ld = D + 4, ldv = 64 * NDV + 4;
-    float *Qs = smem, *Ks = Qs + M * ld, *Vs = Ks + kTile * ld, *Ps = Vs + kTile * ldv;
+    constexpr int BUF = RI == 1 ? 2 : 1;
+    float *Qs = smem, *Ps = Qs + M * ld, *KV = Ps + M * kLdP;
     int t;
     // the last tiles of a sequence see the most keys: start with them
     const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, M, (int)(gridDim.x - 1 - blockIdx.x), &t);
@@ -161,13 +178,23 @@ __global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a) {
 #pragma unroll
     for (int i = 0; i < RI; ++i) m[i] = -INFINITY, l[i] = 0.f;
     const int kend = a.causal ? min(sk.len, r0 + rows + sk.len - sq.len) : sk.len;
+    auto copy = [&](int k0) {
+        float *Ks = KV + (k0 / kTile % BUF) * kTile * (ld + ldv), *Vs = Ks + kTile * ld;
+        const int n = min(kTile, sk.len - k0);
+        copy_rows<kTile, NT>(Ks, ld, (const float *)a.k, a.Dk, (const float *)a.k_shared, a.Ds, 1, sk.start + k0, n, a.H, h);
+        copy_rows<kTile, NT>(Vs, ldv, (const float *)a.v, 64 * NDV, (const float *)nullptr, 0, 1, sk.start + k0, n, a.H, h);
+        cp_async_commit();
+    };
+    if (BUF == 2 && kend > 0) copy(0);
     for (int k0 = 0; k0 < kend; k0 += kTile) {
+        float *Ks = KV + (k0 / kTile % BUF) * kTile * (ld + ldv), *Vs = Ks + kTile * ld;
+        if (BUF == 1) {
+            __syncthreads();
+            copy(k0);
+        }
+        cp_async_wait_all();
         __syncthreads();
-        load_rows<T, kTile, NT>(Ks, ld, (const T *)a.k, a.Dk, (const T *)a.k_shared, a.Ds, 1, sk.start + k0,
-                     min(kTile, sk.len - k0), a.H, h);
-        load_rows<T, kTile, NT>(Vs, ldv, (const T *)a.v, 64 * NDV, (const T *)nullptr, 0, 1, sk.start + k0,
-                     min(kTile, sk.len - k0), a.H, h);
-        __syncthreads();
+        if (BUF == 2 && k0 + kTile < kend) copy(k0 + kTile);
         float s[RI][4] = {};
         dot<RI>(s, Qs, ld, Ks, ld, D);
 #pragma unroll
@@ -351,11 +378,12 @@ __global__ void __launch_bounds__(256) latent_shared_sum_kernel(const float *par
 
 template <typename T, int NDV, int RI, int NT> cudaError_t forward_ri(const LatentArgs &a, cudaStream_t s) {
     constexpr int M = RI * NT / 16;
-    constexpr size_t most = sizeof(float) * (M * (192 + 4 + kLdP) + kTile * ((192 + 4) + (64 * NDV + 4)));
+    constexpr int BUF = RI == 1 ? 2 : 1;
+    constexpr size_t most = sizeof(float) * (M * (192 + 4 + kLdP) + BUF * kTile * ((192 + 4) + (64 * NDV + 4)));
     const cudaError_t e = allow_smem<latent_forward_f32_kernel<T, NDV, RI, NT>>(most);
     if (e != cudaSuccess) return e;
     const int ld = a.Dk + a.Ds + 4;
-    const size_t bytes = sizeof(float) * (M * (ld + kLdP) + kTile * (ld + (64 * NDV + 4)));
+    const size_t bytes = sizeof(float) * (M * (ld + kLdP) + BUF * kTile * (ld + (64 * NDV + 4)));
     const dim3 grid(tile_slots(a.total_q, a.num_seqs, M), a.H);
     latent_forward_f32_kernel<T, NDV, RI, NT><<<grid, NT, bytes, s>>>(a);
     return cudaGetLastError();
