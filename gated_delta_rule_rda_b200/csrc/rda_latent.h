@@ -40,7 +40,7 @@ struct LatentArgs {
     // backward only
     const void *d_out;
     void *dq, *dq_shared, *dk, *dk_shared, *dv;
-    float *delta;                // workspace: sum_d d_out out, [total_q, H]
+    float *delta;                // workspace: sum_d d_out out, [total_q, H] (fp32 forward: parts of split rows)
     float *dks_heads;            // workspace: the shared key part's gradient per head, [total_k, H, Ds]
 };
 
@@ -124,6 +124,7 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s);
 
 size_t latent_backward_scratch_bytes(int total_q, int total_k, int H, int Ds);
+size_t latent_forward_f32_scratch_bytes(int total_q, int total_k, int H, int Dv);
 size_t latent_decode_scratch_bytes(int B, int T, int H, int Dl);
 size_t latent_decode_tc_scratch_bytes(int T, int H, int Dl, int Ds);
 size_t verify_scratch_bytes(int B, int V);

@@ -50,7 +50,8 @@ extern "C" {
 
 size_t rda_latent_prefill_workspace_bytes(int total_q, int total_k, int H, int Dk, int Ds, int Dv, int num_seqs) {
     if (total_q < 0 || total_k < 0 || H <= 0 || H > kMaxHeads || num_seqs < 0 || !head_dims_ok(Dk, Ds, Dv)) return 0;
-    return kErrorWordBytes + latent_prefill_scratch_bytes(total_q, num_seqs);
+    return kErrorWordBytes + std::max(latent_prefill_scratch_bytes(total_q, num_seqs),
+                                      latent_forward_f32_scratch_bytes(total_q, total_k, H, Dv));
 }
 
 rda_status_t rda_latent_prefill(const void *q, const void *q_shared, const void *k, const void *k_shared, const void *v,
@@ -78,6 +79,7 @@ rda_status_t rda_latent_prefill(const void *q, const void *q_shared, const void 
     a.wait_ns = ws.wait_ns;
     a.debug_drop = ws.drop_chunk;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    a.delta = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kErrorWordBytes);
     return done(dtype == RDA_BF16 ? launch_latent_forward_tc(a, static_cast<uint8_t *>(workspace) + kErrorWordBytes, s)
                                   : launch_latent_forward_f32(a, s));
 }

@@ -11,6 +11,7 @@
 // consecutive rows on different banks).
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "rda_io.cuh"
@@ -155,11 +156,12 @@ __device__ __forceinline__ bool seen(const LatentArgs &a, int i, int j, int lq, 
 // Forward: one CTA per (RI NT / 16 query rows, head), online softmax over key
 // tiles.  RI = 4 with 512 threads (128 rows) reads each operand for four products
 // and keeps 16 warps on an SM; RI = 1 with 256 threads (16 rows) makes eight times
-// as many CTAs, for calls that would leave SMs empty, and copies the next key tile
-// while it works on one.
+// as many CTAs, for calls that would leave SMs empty, copies the next key tile
+// while it works on one, and may split the keys over `splits` CTAs (blockIdx.z),
+// whose results a second kernel joins.
 // ---------------------------------------------------------------------------
 template <typename T, int NDV, int RI, int NT>
-__global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a) {
+__global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a, int splits) {
     extern __shared__ __align__(16) float smem[];
     constexpr int M = RI * NT / 16;
     const int D = a.Dk + a.Ds, ld = D + 4, ldv = 64 * NDV + 4;
@@ -185,8 +187,11 @@ __global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a) {
         copy_rows<kTile, NT>(Vs, ldv, (const float *)a.v, 64 * NDV, (const float *)nullptr, 0, 1, sk.start + k0, n, a.H, h);
         cp_async_commit();
     };
-    if (BUF == 2 && kend > 0) copy(0);
-    for (int k0 = 0; k0 < kend; k0 += kTile) {
+    const int all = kend > 0 ? (kend + kTile - 1) / kTile : 0;
+    const int k_lo = RI == 1 ? all * (int)blockIdx.z / splits * kTile : 0;
+    const int k_hi = RI == 1 ? min(kend, all * ((int)blockIdx.z + 1) / splits * kTile) : kend;
+    if (BUF == 2 && k_lo < k_hi) copy(k_lo);
+    for (int k0 = k_lo; k0 < k_hi; k0 += kTile) {
         float *Ks = KV + (k0 / kTile % BUF) * kTile * (ld + ldv), *Vs = Ks + kTile * ld;
         if (BUF == 1) {
             __syncthreads();
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a) {
         }
         cp_async_wait_all();
         __syncthreads();
-        if (BUF == 2 && k0 + kTile < kend) copy(k0 + kTile);
+        if (BUF == 2 && k0 + kTile < k_hi) copy(k0 + kTile);
         float s[RI][4] = {};
         dot<RI>(s, Qs, ld, Ks, ld, D);
 #pragma unroll
@@ -231,13 +236,27 @@ __global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a) {
 #pragma unroll
         for (int off = 8; off; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
         const int r = r0 + RI * ty + i;
-        if (a.lse && tx == 0 && RI * ty + i < rows)
-            a.lse[(size_t)(sq.start + r) * a.H + h] = l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
+        if (tx == 0 && RI * ty + i < rows) {
+            const size_t at = (size_t)(sq.start + r) * a.H + h;
+            const float lse = l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
+            if (RI == 1 && splits > 1) a.delta[at * splits + blockIdx.z] = lse;
+            else if (a.lse) a.lse[at] = lse;
+        }
         const float f = l[i] > 0.f ? 1.f / l[i] : 0.f;
 #pragma unroll
         for (int c = 0; c < NDV; ++c)
 #pragma unroll
             for (int u = 0; u < 4; ++u) o[i][c][u] *= f;
+    }
+    if (RI == 1 && splits > 1) {
+        // a part: [row][split][Dv] behind the log-sum-exps
+        const size_t rows_all = (size_t)a.total_q * a.H, at = ((size_t)(sq.start + r0 + ty) * a.H + h) * splits + blockIdx.z;
+        float *po = a.delta + ((rows_all * splits + 3) & ~(size_t)3) + at * (64 * NDV);
+        if (ty < rows)
+#pragma unroll
+            for (int c = 0; c < NDV; ++c)
+                *reinterpret_cast<float4 *>(po + 64 * c + 4 * tx) = make_float4(o[0][c][0], o[0][c][1], o[0][c][2], o[0][c][3]);
+        return;
     }
     store_rows<T, T, RI, NDV>(o, 1.f, (T *)a.out, 64 * NDV, (T *)nullptr, 0, sq.start + r0, rows, a.H, h);
 }
@@ -376,22 +395,36 @@ __global__ void __launch_bounds__(256) latent_shared_sum_kernel(const float *par
     Io<T>::st4(out + row * Ds + c, x);
 }
 
-template <typename T, int NDV, int RI, int NT> cudaError_t forward_ri(const LatentArgs &a, cudaStream_t s) {
+// Fewer tiles of 64 rows than SMs: tiles of 16, and the keys split until two CTAs per SM have work (8 at most).
+bool forward_few(int total_q, int H) { return (long)(total_q / kTile + 1) * H < 148; }
+int forward_splits(int total_q, int total_k, int H) {
+    if (!forward_few(total_q, H)) return 1;
+    const long ctas = (long)(total_q / 16 + 1) * H, want = 296 / ctas, tiles = (total_k + kTile - 1) / kTile;
+    return (int)std::max(1L, std::min({want, tiles, 8L}));
+}
+
+__global__ void latent_join_kernel(LatentDecodeArgs a, int splits, const int32_t *end);
+
+template <typename T, int NDV, int RI, int NT> cudaError_t forward_ri(const LatentArgs &a, int splits, cudaStream_t s) {
     constexpr int M = RI * NT / 16;
     constexpr int BUF = RI == 1 ? 2 : 1;
     constexpr size_t most = sizeof(float) * (M * (192 + 4 + kLdP) + BUF * kTile * ((192 + 4) + (64 * NDV + 4)));
-    const cudaError_t e = allow_smem<latent_forward_f32_kernel<T, NDV, RI, NT>>(most);
+    cudaError_t e = allow_smem<latent_forward_f32_kernel<T, NDV, RI, NT>>(most);
     if (e != cudaSuccess) return e;
     const int ld = a.Dk + a.Ds + 4;
     const size_t bytes = sizeof(float) * (M * (ld + kLdP) + BUF * kTile * (ld + (64 * NDV + 4)));
-    const dim3 grid(tile_slots(a.total_q, a.num_seqs, M), a.H);
-    latent_forward_f32_kernel<T, NDV, RI, NT><<<grid, NT, bytes, s>>>(a);
+    const dim3 grid(tile_slots(a.total_q, a.num_seqs, M), a.H, splits);
+    latent_forward_f32_kernel<T, NDV, RI, NT><<<grid, NT, bytes, s>>>(a, splits);
+    if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
+    LatentDecodeArgs j{};
+    j.B = a.total_q, j.T = 1, j.H = a.H, j.Dl = 64 * NDV;
+    j.out = a.out, j.lse = a.lse, j.part = a.delta;
+    latent_join_kernel<<<a.total_q * a.H, 128, 0, s>>>(j, splits, a.cu_q + a.num_seqs);
     return cudaGetLastError();
 }
 template <typename T, int NDV> cudaError_t forward_nv(const LatentArgs &a, cudaStream_t s) {
-    // fewer tiles of 64 rows than SMs: tiles of 16
-    const bool few = (long)(a.total_q / kTile + 1) * a.H < 148;
-    return few ? forward_ri<T, NDV, 1, 256>(a, s) : forward_ri<T, NDV, 4, 512>(a, s);
+    if (!forward_few(a.total_q, a.H)) return forward_ri<T, NDV, 4, 512>(a, 1, s);
+    return forward_ri<T, NDV, 1, 256>(a, forward_splits(a.total_q, a.total_k, a.H), s);
 }
 
 template <typename T, int ND, int NDV> cudaError_t backward_nd(const LatentArgs &a, cudaStream_t s) {
@@ -600,8 +633,10 @@ __global__ void __launch_bounds__(16 * ROWS) latent_decode_f32_kernel(LatentDeco
 }
 
 // out = sum_s e^{lse_s - lse} o_s, lse = log sum_s e^{lse_s}: one CTA per row.
-__global__ void __launch_bounds__(128) latent_join_kernel(LatentDecodeArgs a, int splits) {
+// Rows of tokens from *end on (where given) are left as they were.
+__global__ void __launch_bounds__(128) latent_join_kernel(LatentDecodeArgs a, int splits, const int32_t *end) {
     const size_t row = blockIdx.x;
+    if (end && (long)(row / a.H) >= (long)*end) return;
     const float *ls = a.part + row * splits;
     const float *po = a.part + (((size_t)a.B * a.T * a.H * splits + 3) & ~(size_t)3) + row * splits * a.Dl;
     float top = -INFINITY, sum = 0.f;
@@ -639,7 +674,7 @@ template <int NL, int ROWS> cudaError_t decode_rows_nl(const LatentDecodeArgs &a
     const size_t bytes = sizeof(float) * ((ROWS + 2 * kDecTok) * (128 * NL + a.Ds + 4) + extra);
     latent_decode_f32_kernel<NL, ROWS><<<dim3(splits * a.B, (R + ROWS - 1) / ROWS), 16 * ROWS, bytes, s>>>(a, splits);
     if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
-    latent_join_kernel<<<a.B * R, 128, 0, s>>>(a, splits);
+    latent_join_kernel<<<a.B * R, 128, 0, s>>>(a, splits, nullptr);
     return cudaGetLastError();
 }
 template <int NL> cudaError_t decode_nl(const LatentDecodeArgs &a, cudaStream_t s) {
@@ -689,6 +724,11 @@ cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s) 
 size_t latent_backward_scratch_bytes(int total_q, int total_k, int H, int Ds) {
     const size_t d = ((size_t)total_q * H * sizeof(float) + 255) / 256 * 256;
     return d + (size_t)total_k * H * Ds * sizeof(float);
+}
+
+size_t latent_forward_f32_scratch_bytes(int total_q, int total_k, int H, int Dv) {
+    const int splits = forward_splits(total_q, total_k, H);
+    return splits == 1 ? 0 : ((size_t)total_q * H * splits * (Dv + 1) + 4) * sizeof(float);
 }
 
 size_t latent_decode_scratch_bytes(int B, int T, int H, int Dl) {
