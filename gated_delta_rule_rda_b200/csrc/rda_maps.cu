@@ -6,8 +6,8 @@
 
 namespace rda {
 
-static bool encode_bf16(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                        const cuuint32_t *box) {
+bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
+                 uint64_t stride2, uint32_t box1, uint32_t box2) {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -15,29 +15,15 @@ static bool encode_bf16(CUtensorMap *map, const void *base, int rank, const cuui
                         q == cudaDriverEntryPointSuccess;
         return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
     }();
-    const cuuint32_t step[4] = {1, 1, 1, 1};
-    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box,
+    const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {stride1 * 2, stride2 * 2};
+    const cuuint32_t box[3] = {64, box1, box2}, step[3] = {1, 1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
                             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
-                 uint64_t stride2, uint32_t box1, uint32_t box2) {
-    const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {stride1 * 2, stride2 * 2};
-    const cuuint32_t box[3] = {64, box1, box2};
-    return encode_bf16(map, base, 3, dims, strides, box);
-}
-
 bool make_map_heads(CUtensorMap *map, const void *base, int D, int H, long rows, uint32_t box, const void *any) {
     return make_map_3d(map, rows ? base : any, D, H, rows ? rows : 1, D, (uint64_t)H * D, 1, box);
-}
-
-bool make_map_pages(CUtensorMap *map, const void *base, uint64_t cols, uint64_t page_size, uint64_t pages,
-                    uint32_t box_rows, uint32_t chunks) {
-    const cuuint64_t dims[4] = {64, page_size, cols / 64, pages};
-    const cuuint64_t strides[3] = {cols * 2, 128, page_size * cols * 2};
-    const cuuint32_t box[4] = {64, box_rows, chunks, 1};
-    return encode_bf16(map, base, 4, dims, strides, box);
 }
 
 }  // namespace rda

@@ -48,15 +48,6 @@ struct Waiter {
     }
 };
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
-                                            int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
-
 // One lane of a converged warp.  The MMA issuers branch on it (and not on the
 // lane's number): the compiler then knows that one thread runs the branch and
 // keeps descriptors in uniform registers.  An unrolled chain of M = 64, N = 16
@@ -261,9 +252,5 @@ bool make_map_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, u
 // [rows, H, D]: boxes of 64 columns of one head x `box` rows; where there are no rows the map is only read outside
 // its bounds, and `any` is its base.
 bool make_map_heads(CUtensorMap *map, const void *base, int D, int H, long rows, uint32_t box, const void *any);
-// Rows of `cols` bf16 values in pages, as [page][column / 64][row][64]: boxes of `box_rows` rows x `chunks` times 64
-// columns land as `chunks` tiles of 128-byte rows.
-bool make_map_pages(CUtensorMap *map, const void *base, uint64_t cols, uint64_t page_size, uint64_t pages,
-                    uint32_t box_rows, uint32_t chunks);
 
 }  // namespace rda
