@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <utility>
 
 #include "rda_internal.h"
 
@@ -108,6 +109,24 @@ struct TileOrder {
     int2 *out;                   // [slots]: {sequence, tile}, then {-1, -1}
 };
 size_t order_bytes(int total, int num_seqs, int tile);
+
+// A launch whose prologue may overlap the end of the kernel before it on the
+// stream (`overlap`: that kernel lets its dependents go and every CTA of this one
+// waits for it before its first exit, so that whatever comes next finds both done).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, bool overlap, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = overlap ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 cudaError_t launch_latent_forward_f32(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_latent_backward_f32(const LatentArgs &a, cudaStream_t s);

@@ -61,6 +61,7 @@ struct Maps {
 // Two more CTAs (of the row behind the heads) put the tiles of the other kernels in order.
 __global__ void __launch_bounds__(256) latent_stats_kernel(const LatentArgs a, float *stats, const TileOrder rows,
                                                            const TileOrder keys) {
+    pdl_launch_dependents();
     if (blockIdx.y == a.H) {
         if (blockIdx.x < 2) order_tiles(a, blockIdx.x ? keys : rows);
         return;
@@ -143,6 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // heads side by side, tiles with the most work first
     const int h = blockIdx.x % a.H;
+    pdl_launch_dependents();
+    pdl_wait_primary();
     int t;
     const int n = tile_at(a, true, 128, blockIdx.x / a.H, gridDim.x / a.H, &t);
     if (n < 0) return;
@@ -414,6 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Waiter w{&B.abort, a.err, a.wait_ns};
 
     const int h = blockIdx.x % a.H;
+    pdl_launch_dependents();
+    pdl_wait_primary();
     int t;
     const int n = tile_at(a, false, 128, blockIdx.x / a.H, gridDim.x / a.H, &t);
     if (n < 0) return;
@@ -684,14 +689,16 @@ cudaError_t launch_latent_backward_tc(const LatentArgs &a0, void *scratch, cudaS
     if (a.total_q > 0) {
         if (!make_maps(&m, a, 128, kKeys)) return cudaErrorInvalidValue;
         a.order = sorted ? rows.out : nullptr;
-        latent_dq_kernel<<<tile_slots(a.total_q, a.num_seqs, 128) * a.H, kThreads, smem_b(nk, nv), s>>>(m, a, stats, blocks);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_after(latent_dq_kernel, tile_slots(a.total_q, a.num_seqs, 128) * a.H, kThreads, smem_b(nk, nv), s, true, m, a,
+                         stats, blocks);
+        if (e != cudaSuccess) return e;
     }
     if (a.total_k > 0) {
         if (!make_maps(&m, a, kRows, 128)) return cudaErrorInvalidValue;
         a.order = sorted ? keys.out : nullptr;
-        latent_dkv_kernel<<<tile_slots(a.total_k, a.num_seqs, 128) * a.H, kThreads, smem_a(nk, nv), s>>>(m, a, stats, blocks);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_after(latent_dkv_kernel, tile_slots(a.total_k, a.num_seqs, 128) * a.H, kThreads, smem_a(nk, nv), s,
+                         a.total_q > 0 || sorted, m, a, stats, blocks);
+        if (e != cudaSuccess) return e;
     }
     return a.Ds ? launch_latent_shared_sum(a, s) : cudaSuccess;
 }

@@ -785,20 +785,11 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s) {
         default: e = launch<64>(maps, args, s); break;
     }
     if (e != cudaSuccess || args.g.groups == 1) return e;
-    cudaLaunchConfig_t cfg = {};
     // Parts per sequence: about groups / B.  From 16 on a whole CTA per row pays (the parts are read in turn).
     const bool many = args.g.groups >= 16 * a.B;
     const int at = args.g.rt * args.g.rows;
-    cfg.gridDim = dim3(args.g.groups, many ? at : (at + 3) / 4);
-    cfg.blockDim = dim3(kJoin);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, latent_join_bf16_kernel<4>, args)
-                : cudaLaunchKernelEx(&cfg, latent_join_bf16_kernel<1>, args);
+    const dim3 grid(args.g.groups, many ? at : (at + 3) / 4);
+    return launch_after(many ? latent_join_bf16_kernel<4> : latent_join_bf16_kernel<1>, grid, kJoin, 0, s, true, args);
 }
 
 }  // namespace rda

@@ -379,17 +379,7 @@ cudaError_t launch_latent_forward_tc(const LatentArgs &a0, void *scratch, cudaSt
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         a.order = o.out;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(slots * a.H);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = sorted ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_prefill_kernel, m, a);
+    return launch_after(latent_prefill_kernel, slots * a.H, kThreads, bytes, s, sorted, m, a);
 }
 
 }  // namespace rda

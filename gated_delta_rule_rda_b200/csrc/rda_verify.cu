@@ -233,16 +233,7 @@ cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
     else verify_sums_kernel<false><<<grid, 32 * kWarps, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.B);
-    cfg.blockDim = dim3(kPick);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_pick_kernel, a);
+    return launch_after(verify_pick_kernel, a.B, kPick, 0, s, true, a);
 }
 
 }  // namespace rda
