@@ -477,10 +477,11 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
             // roles has to stay in the instruction caches for the MMAs to be issued as fast as they run.
             constexpr uint32_t idS = idesc_bf16(kTok, NT, 0, 0), idO = idesc_bf16(128, NT, 1, 0);
             // descriptors count in units of 16 bytes: offsets are added to the first slot's
-            const uint64_t dq = smem_desc(smem_u32(q_s), 16, 1024, kSw128), dp = smem_desc(smem_u32(p_s), 16, 1024, kSw128);
-            const uint64_t dc = smem_desc(smem_u32(pair_s), 16, 1024, kSw128);
-            const uint64_t dv = smem_desc(smem_u32(pair_s), kBox, 1024, kSw128);
-            const uint64_t ds = smem_desc(smem_u32(shared_s), 16, 1024, kSw128);
+            const uint32_t dq = (uint32_t)smem_desc(smem_u32(q_s), 16, 1024, kSw128), dp = (uint32_t)smem_desc(smem_u32(p_s), 16, 1024, kSw128);
+            const uint32_t dc = (uint32_t)smem_desc(smem_u32(pair_s), 16, 1024, kSw128);
+            const uint32_t dv = (uint32_t)smem_desc(smem_u32(pair_s), kBox, 1024, kSw128);
+            const uint32_t ds = (uint32_t)smem_desc(smem_u32(shared_s), 16, 1024, kSw128);
+            const uint32_t high = (uint32_t)(smem_desc(0, 0, 1024, kSw128) >> 32);
             constexpr uint32_t kQBox = NT * 8, kPairD = kPair / 16, kBoxD = kBox / 16;
             const uint32_t slot_d = g.sp * kPairD;
             RingPos qk_p, pv_p;
@@ -497,10 +498,10 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
                     tc_fence_after();
                     for (int n = 0; n < NS; ++n) {
                         for (int p = 0; p < g.sp; ++p) {
-                            const uint64_t da = dv + (pv_p.slot * slot_d + p * kPairD);
+                            const uint32_t da = dv + (pv_p.slot * slot_d + p * kPairD);
                             const uint32_t d = t_o + (n * g.sp + p) * NT;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) mma_bf16(d, da + k * 128, dp + k * 2, idO, t != walk.t0 || k > 0);
+                            for (int k = 0; k < 4; ++k) mma_bf16_low(d, da + k * 128, dp + k * 2, high, idO, t != walk.t0 || k > 0);
                         }
                         mma_commit(&S.empty[pv_p.slot]);
                         pv_p.next(g.slots);
@@ -519,17 +520,20 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
                     fence_proxy_async_smem();            // the copies wrote through the generic proxy
                     tc_fence_after();
                     const uint32_t d = t_s + (qk_it & 1) * NT;
-                    const uint64_t da = dc + qk_p.slot * slot_d, db = dq + part * 2 * g.sp * kQBox;
-                    for (int c = 0; c < 2 * g.sp; ++c)
+                    const uint32_t da = dc + qk_p.slot * slot_d, db = dq + part * 2 * g.sp * kQBox;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c >= 2 * g.sp) break;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_bf16(d, da + (c * kBoxD + k * 2), db + (c * kQBox + k * 2), idS, part > 0 || c > 0 || k > 0);
+                            mma_bf16_low(d, da + (c * kBoxD + k * 2), db + (c * kQBox + k * 2), high, idS, part > 0 || c > 0 || k > 0);
+                    }
                     qk_p.next(g.slots);
                     if (++part == NS) {
                         if (a.Ds) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_bf16(d, ds + (qk_shared * kBoxD + k * 2), dq + (2 * NP * kQBox + k * 2), idS, 1);
+                                mma_bf16_low(d, ds + (qk_shared * kBoxD + k * 2), dq + (2 * NP * kQBox + k * 2), high, idS, 1);
                             if (++qk_shared == g.shared) qk_shared = 0;
                         }
                         mma_commit(&S.s_full[qk_it & 1]);

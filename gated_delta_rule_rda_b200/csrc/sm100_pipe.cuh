@@ -48,6 +48,18 @@ struct Waiter {
     }
 };
 
+// An MMA whose operands' descriptors are given by their low words (address and leading offset); the high words (stride
+// and swizzle) are the same constant.  Half the arithmetic per MMA for a thread that issues them one after the other.
+__device__ __forceinline__ void mma_bf16_low(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
 // One lane of a converged warp.  The MMA issuers branch on it (and not on the
 // lane's number): the compiler then knows that one thread runs the branch and
 // keeps descriptors in uniform registers.  An unrolled chain of M = 64, N = 16
