@@ -637,6 +637,11 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
                     cp_async_arrive(smem_u32(&S.full[pr.slot]));
                     pr.next(g.slots);
                 }
+                // the next tile's tokens come as far as L2 while this warp waits for room
+                const Walk &then = t + 1 < walk.t1 ? walk : after;
+                const int j1 = (t + 1 < walk.t1 ? t + 1 : after.t0) * kTok + 16 * mine, have1 = min(16, then.len - j1);
+                if ((t + 1 < walk.t1 || another) && lane == 0 && have1 > 0 && page_next >= 0 && page_next < a.num_pages)
+                    prefetch_l2(pages + ((size_t)page_next * a.page_size + j1 % a.page_size) * D, have1 * D * 2);
             }
             walk = after;
             more = more && another;

@@ -60,6 +60,11 @@ __device__ __forceinline__ void mma_bf16_low(uint32_t d, uint32_t a, uint32_t b,
         : "memory");
 }
 
+// `bytes` (a multiple of 16) from a 16-byte boundary on come into L2.
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(p)), "r"(bytes) : "memory");
+}
+
 // One lane of a converged warp.  The MMA issuers branch on it (and not on the
 // lane's number): the compiler then knows that one thread runs the branch and
 // keeps descriptors in uniform registers.  An unrolled chain of M = 64, N = 16
