@@ -46,7 +46,7 @@ using namespace ptx;
 
 constexpr int kTok = 64;                 // tokens per tile
 constexpr int kCtas = 148;               // one CTA per SM
-constexpr int kScan = 192;               // threads that sum up the lengths
+constexpr int kScan = 128;               // threads that sum up the lengths
 constexpr uint32_t kPair = 16384;        // 64 tokens x 128 latent columns; a slot is one or two of them
 constexpr uint32_t kBox = 8192;          // 64 tokens x 64 columns
 constexpr int kMaxSlots = 12, kMaxShared = 2;
@@ -67,10 +67,12 @@ template <int NT> struct Small {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t q_full, q_empty, s_full[2], p_ready, pv_done, o_empty, drained;
     alignas(8) uint16_t seen[kInfo][kCopyWarps];    // which of a tile's tokens are cached, 16 by each copying warp
-    float wmax[4][NT];
-    float lsum[4][NT];
+    union {
+        long long sums[kScan];           // before the roles part
+        float wmax[4][NT];               // within a tile
+        float lsum[4][NT];               // at a segment's end
+    };
     float factor[NT];
-    long long sums[kScan];
     long long total, lo, hi;
     int first_b, first_off;
     int lens[kLens];
@@ -155,9 +157,14 @@ __device__ __forceinline__ void store_result(uint32_t t_o, int NP, int rows, con
             tmem_ld16(t_o + p * NT + c, x);
             tmem_wait_ld();
             T *o = out + c * stride + 128 * p;
+            if (c + 16 <= rows) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i, o += stride)
-                if (c + i < rows) *o = conv(x[i] * f[i]);
+                for (int i = 0; i < 16; ++i) o[i * stride] = conv(x[i] * f[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < rows) o[i * stride] = conv(x[i] * f[i]);
+            }
         }
     }
 }
@@ -318,6 +325,7 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
         }
         // the segment's result: whole, or one part of a sequence
         const bool done = walk.t0 == 0 && walk.t1 == walk.tiles;
+        named_bar_sync(bar, 128);                    // the last maxima are read, lsum takes their place
         const size_t slot = ((size_t)grp * g.rt + rt) * 2 + (first_segment ? 0 : 1);
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -378,10 +386,9 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
 
 template <int NT>
 __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const __grid_constant__ Maps maps, const Args args) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t sm[];      // no room to spare for aligning it here
     const LatentDecodeArgs &a = args.a;
     const Geometry &g = args.g;
-    uint8_t *sm = align_1024(smem_raw);
     const int NP = a.Dl / 128, NB = (a.Dl + a.Ds) / 64, NS = NP / g.sp;    // pairs, boxes, slots of a tile
     uint8_t *q_s = sm, *p_s = q_s + NB * NT * 128, *pair_s = p_s + NT * 128, *shared_s = pair_s + g.slots * g.sp * kPair;
     Small<NT> &S = *reinterpret_cast<Small<NT> *>(shared_s + (a.Ds ? g.shared * kBox : 0));
@@ -390,6 +397,10 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
     const int R = a.T * a.H, row0 = rt * g.rows, rows = min(g.rows, R - row0);
     const Waiter w{&S.abort, a.err, a.wait_ns};
     pdl_launch_dependents();
+    if (smem_u32(sm) & 1023) {                           // the swizzled operands need it
+        if (tid == 0) atomicCAS(a.err, 0, (int32_t)RDA_ERR_CUDA);
+        return;
+    }
     constexpr uint32_t kCols = NT <= 16 ? 128 : NT <= 32 ? 256 : 512;      // 4 NT for O^T, 2 NT for S^T
 
     if (warp == 0) {
@@ -745,7 +756,7 @@ Geometry geometry(int T, int H, int Dl, int Ds) {
     g.nt = (g.rows + 15) / 16 * 16;
     g.groups = std::max(1, kCtas / g.rt);
     const uint32_t small = g.nt == 16 ? small_bytes<16>() : g.nt == 32 ? small_bytes<32>() : g.nt == 48 ? small_bytes<48>() : small_bytes<64>();
-    const uint32_t most = 232448 - 1024 - small;
+    const uint32_t most = 232448 - small;
     const int D = Dl + Ds, NP = Dl / 128;
     // slots of two pairs where the latents have an even number: half the waits for the issuing thread
     g.sp = NP % 2 == 0 ? 2 : 1;
@@ -755,7 +766,7 @@ Geometry geometry(int T, int H, int Dl, int Ds) {
     if (Ds && operand_bytes(g.nt, D, 2 * NP, 2) > most) g.shared = 1;
     const uint32_t beside = operand_bytes(g.nt, D, 0, Ds ? g.shared : 0);
     g.slots = std::min<int>(kMaxSlots, (int)((most - beside) / (g.sp * kPair)));
-    g.smem = beside + g.slots * g.sp * kPair + small + 1024;
+    g.smem = beside + g.slots * g.sp * kPair + small;
     return g;
 }
 static_assert(sizeof(Small<64>) % 8 == 0, "barriers are 8-byte aligned");
