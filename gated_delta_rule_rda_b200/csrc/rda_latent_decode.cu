@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
         fence_mbar_init();
         prefetch_tensormap(&maps.q);
     }
+    pdl_wait_primary();                                  // nothing above reads what another kernel may still write
     // this group's range of the tiles of all sequences
     const int per = (a.B + kScan - 1) / kScan, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     {
@@ -703,6 +704,7 @@ template <int SHARES> __global__ void __launch_bounds__(kJoin) latent_join_bf16_
     const int grp = blockIdx.x, at = SHARES == 4 ? blockIdx.y : blockIdx.y * 4 + group;     // row, by tile
     const int rt = at / g.rows, r = at % g.rows, R = a.T * a.H;
     const bool on = at < g.rt * g.rows && rt * g.rows + r < R;
+    pdl_launch_dependents();
     pdl_wait_primary();
     const int4 rec = parts.rec[grp];
     if (rec.x < 0 || !on) return;
@@ -774,8 +776,7 @@ static_assert(sizeof(Small<64>) % 8 == 0, "barriers are 8-byte aligned");
 template <int NT> cudaError_t launch(const Maps &maps, const Args &args, cudaStream_t s) {
     cudaError_t e = allow_smem<latent_decode_kernel<NT>>(232448);
     if (e != cudaSuccess) return e;
-    latent_decode_kernel<NT><<<args.g.rt * args.g.groups, threads_of(NT), args.g.smem, s>>>(maps, args);
-    return cudaGetLastError();
+    return launch_after(latent_decode_kernel<NT>, args.g.rt * args.g.groups, threads_of(NT), args.g.smem, s, true, maps, args);
 }
 
 }  // namespace

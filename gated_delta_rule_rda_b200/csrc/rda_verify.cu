@@ -112,6 +112,7 @@ template <bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) verify_sums_kernel(VerifyArgs a) {
     const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ptx::pdl_launch_dependents();
+    ptx::pdl_wait_primary();
     int n;
     const int k = kept_drafts(a, b, lane, &n);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.num_accepted[b] = k;
@@ -149,11 +150,12 @@ __global__ void __launch_bounds__(kPick) verify_pick_kernel(VerifyArgs a) {
     __shared__ int slice_s, last_s, token_s, tail_s;
     const int b = blockIdx.x, tid = threadIdx.x;
     if (tid == 0) slice_s = token_s = 0x7fffffff, last_s = tail_s = -1, start_s = 0.0;
-    const int n = a.num_drafts ? min(max(a.num_drafts[b], 0), a.T) : a.T;
-    const double u = a.uniforms[(size_t)b * (a.T + 1) + a.T];
     const int ns = slices_of(a.V);
     double *part = a.part + (size_t)b * ns;
+    ptx::pdl_launch_dependents();
     ptx::pdl_wait_primary();
+    const int n = a.num_drafts ? min(max(a.num_drafts[b], 0), a.T) : a.T;
+    const double u = a.uniforms[(size_t)b * (a.T + 1) + a.T];
     const int k = a.num_accepted[b];
     Rows r = weight_rows(a, b, k, n);
     // each thread's slices are consecutive: one scan gives every slice's start
@@ -229,9 +231,7 @@ cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
     const int rounds = (need + wave - 1) / wave;
     const dim3 grid((need + rounds - 1) / rounds, a.B);
     const bool vec = a.V % 4 == 0 && (uintptr_t)a.target_probs % 16 == 0 && (uintptr_t)a.draft_probs % 16 == 0;
-    if (vec) verify_sums_kernel<true><<<grid, 32 * kWarps, 0, s>>>(a);
-    else verify_sums_kernel<false><<<grid, 32 * kWarps, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(vec ? verify_sums_kernel<true> : verify_sums_kernel<false>, grid, 32 * kWarps, 0, s, true, a);
     if (e != cudaSuccess) return e;
     return launch_after(verify_pick_kernel, a.B, kPick, 0, s, true, a);
 }
