@@ -62,6 +62,7 @@ struct Maps {
 __global__ void __launch_bounds__(256) latent_stats_kernel(const LatentArgs a, float *stats, const TileOrder rows,
                                                            const TileOrder keys) {
     pdl_launch_dependents();
+    pdl_wait_primary();
     if (blockIdx.y == a.H) {
         if (blockIdx.x < 2) order_tiles(a, blockIdx.x ? keys : rows);
         return;
@@ -681,23 +682,23 @@ cudaError_t launch_latent_backward_tc(const LatentArgs &a0, void *scratch, cudaS
     keys.out = rows.out + tile_slots(a.total_q, a.num_seqs, 128);
     const bool sorted = a.num_seqs > 1;           // two CTAs beside the others (blocks >= num_seqs >= 2)
     if (a.total_q > 0 || sorted) {
-        latent_stats_kernel<<<dim3(blocks, a.H + sorted), 256, 0, s>>>(a, stats, rows, keys);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_after(latent_stats_kernel, dim3(blocks, a.H + sorted), 256, 0, s, a, stats, rows, keys);
+        if (e != cudaSuccess) return e;
     }
     Maps m;
     // dQ first: it corrects the statistics that dK uses
     if (a.total_q > 0) {
         if (!make_maps(&m, a, 128, kKeys)) return cudaErrorInvalidValue;
         a.order = sorted ? rows.out : nullptr;
-        e = launch_after(latent_dq_kernel, tile_slots(a.total_q, a.num_seqs, 128) * a.H, kThreads, smem_b(nk, nv), s, true, m, a,
+        e = launch_after(latent_dq_kernel, tile_slots(a.total_q, a.num_seqs, 128) * a.H, kThreads, smem_b(nk, nv), s, m, a,
                          stats, blocks);
         if (e != cudaSuccess) return e;
     }
     if (a.total_k > 0) {
         if (!make_maps(&m, a, kRows, 128)) return cudaErrorInvalidValue;
         a.order = sorted ? keys.out : nullptr;
-        e = launch_after(latent_dkv_kernel, tile_slots(a.total_k, a.num_seqs, 128) * a.H, kThreads, smem_a(nk, nv), s,
-                         a.total_q > 0 || sorted, m, a, stats, blocks);
+        e = launch_after(latent_dkv_kernel, tile_slots(a.total_k, a.num_seqs, 128) * a.H, kThreads, smem_a(nk, nv), s, m, a,
+                         stats, blocks);
         if (e != cudaSuccess) return e;
     }
     return a.Ds ? launch_latent_shared_sum(a, s) : cudaSuccess;

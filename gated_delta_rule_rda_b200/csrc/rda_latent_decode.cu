@@ -776,7 +776,7 @@ static_assert(sizeof(Small<64>) % 8 == 0, "barriers are 8-byte aligned");
 template <int NT> cudaError_t launch(const Maps &maps, const Args &args, cudaStream_t s) {
     cudaError_t e = allow_smem<latent_decode_kernel<NT>>(232448);
     if (e != cudaSuccess) return e;
-    return launch_after(latent_decode_kernel<NT>, args.g.rt * args.g.groups, threads_of(NT), args.g.smem, s, true, maps, args);
+    return launch_after(latent_decode_kernel<NT>, args.g.rt * args.g.groups, threads_of(NT), args.g.smem, s, maps, args);
 }
 
 }  // namespace
@@ -810,7 +810,7 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s) {
     const bool many = args.g.groups >= 16 * a.B;
     const int at = args.g.rt * args.g.rows;
     const dim3 grid(args.g.groups, many ? at : (at + 3) / 4);
-    return launch_after(many ? latent_join_bf16_kernel<4> : latent_join_bf16_kernel<1>, grid, kJoin, 0, s, true, args);
+    return launch_after(many ? latent_join_bf16_kernel<4> : latent_join_bf16_kernel<1>, grid, kJoin, 0, s, args);
 }
 
 }  // namespace rda

@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(256) latent_delta_kernel(const T *out, const T
 template <typename T>
 __global__ void __launch_bounds__(256) latent_shared_sum_kernel(const float *parts, T *out, const int32_t *cu_k,
                                                                 int num_seqs, long rows, int H, int Ds) {
+    ptx::pdl_launch_dependents();
     ptx::pdl_wait_primary();
     const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
     const long row = e / Ds;
@@ -705,7 +706,7 @@ cudaError_t launch_latent_shared_sum(const LatentArgs &a, cudaStream_t s) {
         latent_shared_sum_kernel<float><<<grid, 256, 0, s>>>(a.dks_heads, (float *)a.dk_shared, a.cu_k, a.num_seqs,
                                                              a.total_k, a.H, a.Ds);
     else
-        return launch_after(latent_shared_sum_kernel<__nv_bfloat16>, grid, 256, 0, s, true, (const float *)a.dks_heads,
+        return launch_after(latent_shared_sum_kernel<__nv_bfloat16>, grid, 256, 0, s, (const float *)a.dks_heads,
                             (__nv_bfloat16 *)a.dk_shared, a.cu_k, a.num_seqs, (long)a.total_k, a.H, a.Ds);
     return cudaGetLastError();
 }

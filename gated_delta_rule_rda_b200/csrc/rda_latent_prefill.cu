@@ -75,7 +75,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
     const Waiter w{&B.abort, a.err, a.wait_ns};
 
     // heads side by side, tiles with the most work first
-    if (a.order) pdl_wait_primary();
+    pdl_launch_dependents();
+    pdl_wait_primary();
     const int h = blockIdx.x % a.H;
     int t;
     const int n = tile_at(a, false, kQ * kBM, blockIdx.x / a.H, gridDim.x / a.H, &t);
@@ -347,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
 
 __global__ void __launch_bounds__(512) latent_order_kernel(const LatentArgs a, const TileOrder o) {
     pdl_launch_dependents();
+    pdl_wait_primary();
     order_tiles(a, o);
 }
 
@@ -375,11 +377,10 @@ cudaError_t launch_latent_forward_tc(const LatentArgs &a0, void *scratch, cudaSt
     const bool sorted = a.num_seqs > 1 && (long)slots * a.H > 148;
     if (sorted) {
         TileOrder o{0, kQ * kBM, kBN, static_cast<int2 *>(scratch)};
-        latent_order_kernel<<<1, 512, 0, s>>>(a, o);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_after(latent_order_kernel, 1, 512, 0, s, a, o)) != cudaSuccess) return e;
         a.order = o.out;
     }
-    return launch_after(latent_prefill_kernel, slots * a.H, kThreads, bytes, s, sorted, m, a);
+    return launch_after(latent_prefill_kernel, slots * a.H, kThreads, bytes, s, m, a);
 }
 
 }  // namespace rda

@@ -231,9 +231,9 @@ cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
     const int rounds = (need + wave - 1) / wave;
     const dim3 grid((need + rounds - 1) / rounds, a.B);
     const bool vec = a.V % 4 == 0 && (uintptr_t)a.target_probs % 16 == 0 && (uintptr_t)a.draft_probs % 16 == 0;
-    const cudaError_t e = launch_after(vec ? verify_sums_kernel<true> : verify_sums_kernel<false>, grid, 32 * kWarps, 0, s, true, a);
+    const cudaError_t e = launch_after(vec ? verify_sums_kernel<true> : verify_sums_kernel<false>, grid, 32 * kWarps, 0, s, a);
     if (e != cudaSuccess) return e;
-    return launch_after(verify_pick_kernel, a.B, kPick, 0, s, true, a);
+    return launch_after(verify_pick_kernel, a.B, kPick, 0, s, a);
 }
 
 }  // namespace rda
