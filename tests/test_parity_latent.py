@@ -348,6 +348,59 @@ def test_streams_and_graphs(cuda_device):
     assert torch.equal(od, ed) and torch.equal(ld, eld)
 
 
+def test_calls_wait_for_what_came_before(cuda_device):
+    """Inputs written right before each call, by kernels and by copies, on the same buffers and the same workspace:
+    eager, and in two captured graphs that share the workspace, with a branch that joins before the calls."""
+    pre = [dev(packed([300, 40, 129], [300, 40, 129], 4, 128, 64, 128, BF16, seed=70 + i)) for i in range(2)]
+    dec = [dev(paged([700, 90, 1], 2, 16, 512, 64, 16, BF16, seed=80 + i)) for i in range(2)]
+    names = ("q", "k", "v", "q_shared", "k_shared", "d_out")
+    ws = rda.new_workspace(1 << 27, "cuda")
+
+    def calls(a, b):
+        o, l = forward(a, workspace=ws)
+        g = gradients(a, o, l, workspace=ws)
+        od, ld = absorbed(b, workspace=ws)
+        return [o, l, *(g[n] for n in sorted(g)), od, ld]
+
+    ref = [calls(a, b) for a, b in zip(pre, dec)]
+    torch.cuda.synchronize()
+    a = {n: t.clone() if isinstance(t, torch.Tensor) else t for n, t in pre[0].items()}
+    b = {n: t.clone() if isinstance(t, torch.Tensor) else t for n, t in dec[0].items()}
+    pinned = [x["lens"].cpu().pin_memory() for x in dec]
+
+    def fill(i, by_kernel):
+        for n in names:
+            torch.mul(pre[i][n], 1, out=a[n]) if by_kernel else a[n].copy_(pre[i][n])
+        for n in ("q", "pages", "table", "q_shared"):
+            b[n].zero_()
+            torch.mul(dec[i][n], 1, out=b[n]) if by_kernel else b[n].copy_(dec[i][n])
+        b["lens"].copy_(pinned[i], non_blocking=True)
+
+    got = []
+    for i in range(12):
+        fill(i % 2, i % 4 < 2)
+        got.append(calls(a, b))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, ref[i % 2])), i
+    graphs = []
+    side = torch.cuda.Stream()
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                fill(i, i == 0)
+            main.wait_stream(side)
+            out = calls(a, b)
+        graphs.append((graph, out))
+    for i in (0, 1, 1, 0, 1, 0):
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(graphs[i][1], ref[i])), i
+
+
 def test_binding_refusals(cuda_device):
     x = dev(packed([10], [10], 2, 64, 64, 64, BF16, seed=60))
     with pytest.raises(ValueError):

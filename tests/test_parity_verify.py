@@ -105,6 +105,22 @@ def test_graph_and_streams(cuda_device):
         assert torch.equal(t, tok) and torch.equal(a, acc)
 
 
+def test_calls_wait_for_what_came_before(cuda_device):
+    """Inputs written right before each call, on the same buffers and the same workspace."""
+    sets = [inputs(4, 3, 3001, seed=20 + i) for i in range(3)]
+    ref = [latent.verify(*(t.cpu() for t in s)) for s in sets]
+    sets = [[t.cuda() for t in s] for s in sets]
+    buf = [torch.empty_like(t) for t in sets[0]]
+    ws = rda.new_workspace(rda.rda_verify_drafts_workspace_bytes(4, 3, 3001), "cuda")
+    got = []
+    for i in range(12):
+        for b, t in zip(buf, sets[i % 3]):
+            b.copy_(t) if i % 2 else torch.mul(t, 1, out=b)
+        got.append(rda.rda_verify_drafts(*buf, workspace=ws))
+    for i, (tok, acc) in enumerate(got):
+        assert (tok.cpu().tolist(), acc.cpu().tolist()) == ref[i % 3]
+
+
 def test_a_speculative_step(cuda_device):
     """A hybrid's serving step as it would be used: the prompt through both kinds of layer, its latents into
     pages, drafted tokens through both kinds in one pass each, verification, and the recurrent state taken back
