@@ -244,6 +244,15 @@ def test_decode_dims_and_pages(cuda_device, dtype, Dl, Ds, page):
     assert rda.rda_read_device_error(ws) == 0
 
 
+@pytest.mark.parametrize("T,H", [(5, 16), (2, 33), (1, 80), (3, 27), (8, 12)])
+@pytest.mark.parametrize("Dl,Ds,page", [(512, 64, 16), (512, 0, 64), (384, 64, 32), (256, 64, 64), (128, 64, 16)])
+def test_decode_more_rows_than_a_tile(cuda_device, T, H, Dl, Ds, page):
+    """More than 64 rows are split over CTAs, evenly and not."""
+    x = paged([300, 8, 1000, 64], T, H, Dl, Ds, page, BF16, seed=T + H + Dl)
+    out, lse = absorbed(dev(x))
+    check_absorbed(x, out, lse, BF16)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_decode_bad_pages_and_lengths(cuda_device, dtype):
     """Pages outside the cache drop their tokens, lengths are cut, and the error word says so."""
