@@ -16,8 +16,14 @@
 // In both, one thread issues the first two products and another those that P and
 // dS go into, each as soon as its own operands are there, so that the tensor pipe
 // and the eight element-wise warps (a lane per key, or per query row; two warps
-// share the columns of a lane) work at the same time.  P and dS are rounded to bf16 for their products; p,
-// dp, delta and all sums are fp32.
+// share the columns of a lane) work at the same time.  P and dS are rounded to
+// bf16 for their products; p, dp, delta and all sums are fp32.
+//
+// Measured, 16 heads of 128 + 64 and 128, T = 4096, causal: dQ 122 us, dK and dV 146
+// us, statistics 10 us, the sum 7 us (335 us a call in a loop under the power cap).  A
+// step of the keys kernel takes 1,980 cycles, its MMAs 1,620; one of the rows kernel
+// 2,030 and 1,530.  96 keys a step in two stages measured 181 us for dQ: the third
+// stage of K is worth more than the longer step.
 //
 // The key part that all heads share gets its gradient from every head: the
 // heads' parts are written in fp32 and summed in a fixed order afterwards.

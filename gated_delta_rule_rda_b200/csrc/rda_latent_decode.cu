@@ -9,11 +9,13 @@
 // about R = 100 rows.
 //
 // The few rows are the N of the tensor-core products, the cache their M:
-//   S^T [64 tokens x N]  = C [64 x D] Q^T            (C K-major, as TMA brings it)
+//   S^T [64 tokens x N]  = C [64 x D] Q^T            (C K-major, rows as they lie in a page)
 //   O^T [Dl x N]        += L^T [Dl x 64] P^T          (the same tile, MN-major)
 // so that 16 rows cost 16 columns and not a padded tile of 128.  Tiles are 64
-// tokens: with the latents as 16 KiB slots (64 tokens x 128 columns) the ring
-// holds two to three tiles next to Q, and loads go on while one is worked on.
+// tokens: with the latents as 16 KiB pairs of chunks (64 tokens x 128 columns) the
+// ring holds two to three tiles next to Q, and copies go on while one is worked on.
+// More than 64 rows go to several CTAs, each of which reads the cache (the later
+// ones from L2).
 //
 // Work is split evenly whatever the lengths: the tiles of all sequences, laid
 // end to end, are cut into one contiguous range per CTA (persistent, one CTA per
@@ -21,16 +23,33 @@
 // partial results (normalised, with their log-sum-exp), which a second kernel
 // joins in a fixed order.
 //
-//   warp 0      producer: pages by TMA (one box per 16..64 rows of a page), Q
-//   warp 1      one thread issues the MMAs: the next tile's scores before this
-//               tile's values, so that the tensor pipe works while softmax runs
-//   warps 2..   softmax, four warps (16 rows) or eight (each four take half of the rows): running maximum and sum per row (a column of S^T: over
+//   warp 0      one thread issues the MMAs: whatever can go next, a slot's share of
+//               the next tile's scores or this tile's values, so that the tensor
+//               pipe works while softmax runs
+//   warps 1..4  copies: 16 tokens of a tile each, 512 bytes of a row at a time
+//               (cp.async; pages are multiples of 16 tokens, so a warp's tokens lie
+//               on one page); the tile after that is asked into L2 meanwhile
+//   warps 5..   softmax, four warps (16 rows) or eight (each four take half of the
+//               rows): running maximum and sum per row (a column of S^T: over
 //               lanes by shuffles, over warps through shared memory); P^T goes to
 //               shared memory; O^T stays in TMEM and is rescaled only when a
 //               maximum has grown by more than 2^8
+//   last warp   Q of each sequence by TMA
 //
 // P is rounded to bf16 for its product (its scale is that of the running
 // maximum, its relative error 2^-8 at most); sums and statistics are fp32.
+//
+// Measured (Dl + Ds = 512 + 64, 16 heads; this kernel, without the join's 5 to 8 us):
+//   256 sequences of up to 4096 tokens, 16 rows     106 us, 5.8 TB/s (88% of a copy's rate)
+//   32 of up to 8192, 8 tokens: 128 rows, two CTAs   78 us; what bounds it is how long a
+//               tile stays in the ring, which holds two beside 64 rows of Q: 3,300 cycles a
+//               tile, of which the MMAs take 1,950
+// Copies by TMA took one box per page and chunk, ~200 cycles each whatever its size:
+// 110 us instead of 95 at that time for pages of 32.  Slots of one pair instead of two
+// cost the issuing thread twice the waits (158 us instead of 115 for 256 sequences),
+// slots of four leave no copy in flight; eight copying warps measured 134 us against
+// 115 for four; 65 to 80 rows as one tile of 80 (less than two tiles fit beside it)
+// 60 us against 52 as two of 40.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -692,7 +711,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
 // Joins the parts of the sequence that begins in group blockIdx.x and goes on in
 // others: out = sum_i e^{lse_i - lse} o_i.  128 threads per row and share of the
 // parts: SHARES = 4 takes a row per CTA, each quarter of it every fourth part;
-// SHARES = 1 takes four rows per CTA.
+// SHARES = 1 takes four rows per CTA.  The parts come from L2: 3 to 6 us.
 constexpr int kJoin = 512;
 template <int SHARES> __global__ void __launch_bounds__(kJoin) latent_join_bf16_kernel(const Args args) {
     __shared__ float4 acc_s[SHARES][128];
