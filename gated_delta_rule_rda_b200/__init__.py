@@ -28,6 +28,7 @@ Functions mirror the C entry points of ``include/rda.h``:
 The raw ctypes handle is :data:`lib` (``lib.rda_prefill_chunked(...)`` takes
 plain pointers and sizes, including host-pointer use for the varlen schedule).
 """
+import contextlib
 import ctypes
 import os
 
@@ -481,6 +482,15 @@ def _launch(fn, dev, stream, *args):
         raise RdaError(code, fn.__name__)
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _allocating_on(stream):
+    """Within it, new memory belongs to the stream that the call runs on: it is not handed to
+    anyone else before that stream has got there."""
+    return _NO_CONTEXT if stream is None else torch.cuda.stream(stream)
+
+
 def _latent_sizes(q, k, v, q_shared, k_shared, cu_q, cu_k):
     """Checks the inputs of the expanded form; returns (total_q, total_k, H, Dk, Ds, Dv, N)."""
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or cu_q.dim() != 1 or cu_q.numel() < 1:
@@ -522,16 +532,17 @@ def rda_latent_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, scale, q_sha
         cu_seqlens_k = cu_seqlens_q
     total_q, total_k, H, Dk, Ds, Dv, N = sizes = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
     dev = _device_of(q)
-    if out is None:
-        out = q.new_empty((total_q, H, Dv))
-    else:
+    if out is not None:
         _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
     if lse is not None:
         _need_like(lse, "lse", (total_q, H), torch.float32, dev)
-    elif return_lse:
-        lse = q.new_empty((total_q, H), dtype=torch.float32)
-    if workspace is None:
-        workspace = new_workspace(rda_latent_prefill_workspace_bytes(*sizes), q.device)
+    with _allocating_on(stream):
+        if out is None:
+            out = q.new_empty((total_q, H, Dv))
+        if lse is None and return_lse:
+            lse = q.new_empty((total_q, H), dtype=torch.float32)
+        if workspace is None:
+            workspace = new_workspace(rda_latent_prefill_workspace_bytes(*sizes), q.device)
     _launch(lib.rda_latent_prefill, dev, stream, _addr(q), _addr(q_shared), _addr(k), _addr(k_shared), _addr(v),
             _addr(cu_seqlens_q), _addr(cu_seqlens_k), N, total_q, total_k, _addr(out), _addr(lse), _dtype_code(q),
             H, Dk, Ds, Dv, float(scale), int(bool(causal)), *_scratch(workspace, dev))
@@ -551,11 +562,12 @@ def rda_latent_backward(q, k, v, out, lse, d_out, cu_seqlens_q, cu_seqlens_k=Non
     _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
     _need_like(d_out, "d_out", (total_q, H, Dv), q.dtype, dev)
     _need_like(lse, "lse", (total_q, H), torch.float32, dev)
-    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-             dq_shared=torch.empty_like(q_shared) if Ds else None,
-             dk_shared=torch.empty_like(k_shared) if Ds else None)
-    if workspace is None:
-        workspace = new_workspace(rda_latent_backward_workspace_bytes(*sizes), q.device)
+    with _allocating_on(stream):
+        g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+                 dq_shared=torch.empty_like(q_shared) if Ds else None,
+                 dk_shared=torch.empty_like(k_shared) if Ds else None)
+        if workspace is None:
+            workspace = new_workspace(rda_latent_backward_workspace_bytes(*sizes), q.device)
     _launch(lib.rda_latent_backward, dev, stream, _addr(q), _addr(q_shared), _addr(k), _addr(k_shared), _addr(v),
             _addr(out), _addr(lse), _addr(d_out), _addr(cu_seqlens_q), _addr(cu_seqlens_k), N, total_q, total_k,
             _addr(g["dq"]), _addr(g["dq_shared"]), _addr(g["dk"]), _addr(g["dk_shared"]), _addr(g["dv"]),
@@ -585,16 +597,17 @@ def rda_latent_decode(q, pages, block_table, seq_lens, *, scale, q_shared=None, 
     _need_like(pages, "pages", (num_pages, page_size, Dl + Ds), dt, dev)
     _need_like(block_table, "block_table", (B, block_table.shape[1]), torch.int32, dev)
     _need_like(seq_lens, "seq_lens", (B,), torch.int32, dev)
-    if out is None:
-        out = q.new_empty((B, T, H, Dl))
-    else:
+    if out is not None:
         _need_like(out, "out", (B, T, H, Dl), dt, dev)
     if lse is not None:
         _need_like(lse, "lse", (B, T, H), torch.float32, dev)
-    elif return_lse:
-        lse = q.new_empty((B, T, H), dtype=torch.float32)
-    if workspace is None:
-        workspace = new_workspace(rda_latent_decode_workspace_bytes(B, T, H, Dl, Ds), q.device)
+    with _allocating_on(stream):
+        if out is None:
+            out = q.new_empty((B, T, H, Dl))
+        if lse is None and return_lse:
+            lse = q.new_empty((B, T, H), dtype=torch.float32)
+        if workspace is None:
+            workspace = new_workspace(rda_latent_decode_workspace_bytes(B, T, H, Dl, Ds), q.device)
     _launch(lib.rda_latent_decode, dev, stream, _addr(q), _addr(q_shared), _addr(pages), _addr(block_table),
             _addr(seq_lens), _addr(out), _addr(lse), code, B, T, H, Dl, Ds, num_pages, page_size,
             block_table.shape[1], float(scale), *_scratch(workspace, dev))
@@ -621,16 +634,17 @@ def rda_verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, nu
         _need_like(draft_probs, "draft_probs", (B, T, V), torch.float32, dev)
     if num_drafts is not None:
         _need_like(num_drafts, "num_drafts", (B,), torch.int32, dev)
-    if tokens is None:
-        tokens = draft_tokens.new_empty((B, T + 1))
-    else:
+    if tokens is not None:
         _need_like(tokens, "tokens", (B, T + 1), torch.int32, dev)
-    if num_accepted is None:
-        num_accepted = draft_tokens.new_empty((B,))
-    else:
+    if num_accepted is not None:
         _need_like(num_accepted, "num_accepted", (B,), torch.int32, dev)
-    if workspace is None:
-        workspace = new_workspace(rda_verify_drafts_workspace_bytes(B, T, V), target_probs.device)
+    with _allocating_on(stream):
+        if tokens is None:
+            tokens = draft_tokens.new_empty((B, T + 1))
+        if num_accepted is None:
+            num_accepted = draft_tokens.new_empty((B,))
+        if workspace is None:
+            workspace = new_workspace(rda_verify_drafts_workspace_bytes(B, T, V), target_probs.device)
     _launch(lib.rda_verify_drafts, dev, stream, _addr(draft_tokens), _addr(draft_probs), _addr(target_probs),
             _addr(uniforms), _addr(num_drafts), _addr(tokens), _addr(num_accepted), B, T, V, *_scratch(workspace, dev))
     return tokens, num_accepted

@@ -26,6 +26,7 @@ rda_status_t check_packed(const void *q, const void *q_shared, const void *k, co
     if (num_seqs < 0 || total_q < 0 || total_k < 0 || H <= 0) return RDA_ERR_INVALID_ARG;
     if (!head_dims_ok(Dk, Ds, Dv) || H > kMaxHeads) return RDA_ERR_UNSUPPORTED;
     if ((long long)std::max(total_q, total_k) * H * (Dk + Ds) >= (1LL << 31)) return RDA_ERR_INVALID_ARG;
+    if (((long long)std::max(total_q, total_k) + num_seqs) * H >= (1LL << 31)) return RDA_ERR_INVALID_ARG;      // CTAs
     if ((q_shared == nullptr && total_q > 0) != (Ds == 0 && total_q > 0)) return RDA_ERR_INVALID_ARG;
     if ((k_shared == nullptr && total_k > 0) != (Ds == 0 && total_k > 0)) return RDA_ERR_INVALID_ARG;
     if (num_seqs > 0 && (!cu_q || !cu_k)) return RDA_ERR_INVALID_ARG;
@@ -149,7 +150,7 @@ rda_status_t rda_latent_decode(const void *q, const void *q_shared, const void *
         page_size % 16)
         return RDA_ERR_UNSUPPORTED;
     if ((long long)B * T * H * (Dl + Ds) >= (1LL << 31) || (long long)num_pages * page_size >= (1LL << 31) ||
-        (long long)table_width * page_size >= (1LL << 31))
+        (long long)table_width * page_size >= (1LL << 31) - 1024)     // tokens are counted in int, tiles rounded up
         return RDA_ERR_INVALID_ARG;
     if (B > 0 && T > 0) {
         if (!q || (q_shared == nullptr) != (Ds == 0) || !seq_lens || !out) return RDA_ERR_INVALID_ARG;

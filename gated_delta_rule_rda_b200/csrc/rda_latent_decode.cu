@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
     const Waiter w{&S.abort, a.err, a.wait_ns};
     pdl_launch_dependents();
     if (smem_u32(sm) & 1023) {                           // the swizzled operands need it
+        pdl_wait_primary();
         if (tid == 0) atomicCAS(a.err, 0, (int32_t)RDA_ERR_CUDA);
         return;
     }

@@ -427,7 +427,8 @@ rda_status_t rda_prefill_chunked_noalloc(const void *q, const void *k, const voi
  *                  total_q, total_k (values are kept inside these bounds).  Rows
  *                  behind the last sequence are neither read into a result nor written
  *   lse            device fp32 [total_q,H] or NULL
- *   Dk, Dv in {64, 128}, Ds in {0, 64}, H <= 1024; total * H * (Dk + Ds) < 2^31
+ *   Dk, Dv in {64, 128}, Ds in {0, 64}, H <= 1024; total * H * (Dk + Ds) and
+ *                  (total + num_seqs) * H below 2^31
  * A device-side wait that runs out records RDA_ERR_TIMEOUT as in the prefill calls.
  * Preconditions, not checked: finite inputs within the sequences.  Sums, softmax
  * statistics and (for fp32) products are fp32; bf16 inputs run on the tensor cores,
@@ -479,8 +480,8 @@ rda_status_t rda_latent_backward(const void *q, const void *q_shared, const void
  *   seq_lens     device int32 [B]
  *   lse          device fp32 [B,T,H] or NULL
  *   Dl in {128, 256, 384, 512}, Ds in {0, 64}, page_size a multiple of 16, H <= 1024, B <= 65535;
- *   num_pages * page_size and table_width * page_size below 2^31 (the cache may have more
- *   than 2^31 elements)
+ *   num_pages * page_size below 2^31 (the cache may have more than 2^31 elements),
+ *   table_width * page_size below 2^31 - 1024
  * A page number outside [0, num_pages) takes its tokens out of the sequence, and a
  * length outside [0, table_width * page_size] is cut to it; either records
  * RDA_ERR_INVALID_ARG in the workspace error word.

@@ -110,3 +110,10 @@ def test_binding_refuses_cpu_tensors():
     with pytest.raises(ValueError):
         rda.rda_latent_decode(torch.zeros(1, 1, 2, 128), torch.zeros(2, 16, 128), torch.zeros(1, 2, dtype=torch.int32),
                               torch.zeros(1, dtype=torch.int32), scale=1.0)
+
+
+def test_sizes_that_pass_32_bits_are_refused():
+    for call in (prefill, backward):
+        assert call(n=(1 << 31) - 1) == INVALID and call(n=1 << 21, H=1024) == INVALID
+    assert decode(w=(1 << 25) - 1, ps=64) == INVALID          # rounding the length up to tiles would pass 2^31
+    assert decode(w=(1 << 31) - 1, ps=1 << 30) == INVALID

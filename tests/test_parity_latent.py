@@ -410,6 +410,44 @@ def test_calls_wait_for_what_came_before(cuda_device):
         assert all(torch.equal(x, y) for x, y in zip(graphs[i][1], ref[i])), i
 
 
+def test_memory_made_for_a_call_on_another_stream(cuda_device):
+    """`stream=` another than the current one: results and workspaces made by the call stay whole while the
+    current stream allocates and writes."""
+    a = dev(packed([500, 260], [500, 260], 8, 128, 64, 128, BF16, seed=90))
+    b = dev(paged([3000, 90], 2, 16, 512, 64, 64, BF16, seed=91))
+    ref = [*forward(a), *absorbed(b)]
+    rg = gradients(a, ref[0], ref[1])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        o = [*forward(a, stream=s), *absorbed(b, stream=s)]
+        g = gradients(a, o[0], o[1], stream=s)
+        got.append((o, g))
+        for n in (1 << 12, 1 << 16, 1 << 20, 1 << 22, 1 << 24):
+            torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for o, g in got:
+        assert all(torch.equal(x, y) for x, y in zip(o, ref)) and all(torch.equal(g[n], rg[n]) for n in g)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_scales_that_are_not_positive(cuda_device, dtype, scale):
+    x = packed([150, 40], [150, 90], 2, 128, 64, 128, dtype, seed=92)
+    x["scale"] = scale
+    out, lse = forward(dev(x))
+    r, rg = oracle_forward(x, True), oracle_gradients(x, True)
+    check(out, r["out"], r["out_round"], dtype, 192, scale, 150, "out")
+    check_lse(lse, r["lse"], 192, scale)
+    g = gradients(dev(x), out, lse)
+    for n in ("dq", "dk", "dv", "dq_shared", "dk_shared"):
+        check(g[n], rg[n], rg[n + "_round"], dtype, 192, scale, 3 * 240, n)
+    y = paged([100, 30], 2, 16, 512, 64, 16, dtype, seed=93, scale=scale)
+    out, lse = absorbed(dev(y))
+    check_absorbed(y, out, lse, dtype)
+
+
 def test_binding_refusals(cuda_device):
     x = dev(packed([10], [10], 2, 64, 64, 64, BF16, seed=60))
     with pytest.raises(ValueError):
