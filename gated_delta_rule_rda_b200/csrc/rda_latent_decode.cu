@@ -653,9 +653,16 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
                         }
                     } else {
                         const int half = lane >> 4, y = lane & 15;
-                        for (int r = half; r < 16; r += 2)
-                            cp_async16_or_zero(dst + (y >> 3) * kBox + sw128(16 * mine + r, y & 7),
-                                               src + (size_t)min(r, max(have - 1, 0)) * D + n * 128 + y * 8, r < have ? 16 : 0);
+                        const __nv_bfloat16 *x = src + half * D + n * 128 + y * 8;
+                        const uint32_t to = dst + (y >> 3) * kBox + 16 * mine * 128;
+                        if (have == 16) {
+#pragma unroll
+                            for (int r = 0; r < 16; r += 2, x += 2 * D) cp_async16_row(to + sw128(r + half, y & 7), x);
+                        } else {
+                            for (int r = half; r < 16; r += 2)
+                                cp_async16_or_zero(to + sw128(r, y & 7), src + (size_t)min(r, max(have - 1, 0)) * D + n * 128 + y * 8,
+                                                   r < have ? 16 : 0);
+                        }
                     }
                     if (with) {
 #pragma unroll
