@@ -112,28 +112,6 @@ __device__ __forceinline__ void rows_times(float (&acc)[RI][NC][4], const float 
             }
     }
 }
-// acc[i][4 c ..] += sum_r w[r][4 ty + i] b[r][64 c + 4 tx ..]   (the transpose of w)
-template <int NC>
-__device__ __forceinline__ void cols_times(float (&acc)[4][NC][4], const float *w, const float *b, int ldb) {
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll 4
-    for (int r = 0; r < kTile; ++r) {
-        const float4 x = *reinterpret_cast<const float4 *>(w + r * kLdP + 4 * ty);
-        const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const float4 y = *reinterpret_cast<const float4 *>(b + r * ldb + 64 * c + 4 * tx);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[i][c][0] = fmaf(xs[i], y.x, acc[i][c][0]);
-                acc[i][c][1] = fmaf(xs[i], y.y, acc[i][c][1]);
-                acc[i][c][2] = fmaf(xs[i], y.z, acc[i][c][2]);
-                acc[i][c][3] = fmaf(xs[i], y.w, acc[i][c][3]);
-            }
-        }
-    }
-}
-
 // Columns [64 c, 64 c + 64) of 64 rows to out ([rows, H, D0]) or, from column
 // D0 on, to shared ([rows, H, D1]).
 template <typename T, typename U, int RI, int NC>
@@ -269,103 +247,156 @@ __global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a, in
 }
 
 // ---------------------------------------------------------------------------
-// Gradients.  Two kernels, each with the sums that its CTA owns in registers
-// (keys, or query rows), so that no sum depends on the order of atomics; the
-// price is that the scores and do . v are formed twice.
+// Gradients.  One kernel for both sides: a CTA owns 16 RI rows of the one side
+// (keys: dk, dv; or query rows: dq) with their sums in registers, and walks over
+// the other side's rows that they meet, 32 at a time, the next 32 copied
+// meanwhile.  No sum depends on the order of atomics; the price is that the
+// scores and do . v are formed twice.
+//
+//   w[own][other] = ds (and p for keys):  acc[own] += w[own][..] other's rows
+//
+// 4 x 8 lanes a warp: with RI = 4 a thread's products over four columns read six
+// 128-byte rows of shared memory for 32 FMAs a lane, its sums 16 for 192.  RI = 2
+// makes twice the CTAs, where 64 rows each would leave SMs empty.
+// Measured (16 heads of 128 + 64 and 128, T = 900, causal): @@
 // ---------------------------------------------------------------------------
+constexpr int kMov = 32, kLdW = 40;
 
-// p and ds of the 64 x 64 tile (rows r0.., keys k0..) into Ps and Ss [row][key].
-// Rows and keys outside the sequence, and masked pairs, give zeros.
-__device__ __forceinline__ void tile_grads(const LatentArgs &a, const float *Qs, const float *Ks, int ld, int D,
-                                           const float *Os, const float *Vs, int ldv, int Dv, const float *lse_s,
-                                           const float *delta_s, int r0, int k0, int lq, int lk, float *Ps, float *Ss) {
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float s[4][4] = {}, dp[4][4] = {};
-    dot<4>(s, Qs, ld, Ks, ld, D);
-    dot<4>(dp, Os, ldv, Vs, ldv, Dv);
+// acc[i][j] = a[16 i] . b[16 j], rows of ld floats, over D
+template <int RI>
+__device__ __forceinline__ void dot_rows(float (&acc)[RI][2], const float *a, const float *b, int ld, int D) {
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+        float4 x[RI], y[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+        for (int i = 0; i < RI; ++i) x[i] = *reinterpret_cast<const float4 *>(a + 16 * i * ld + d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool on = seen(a, r0 + r, k0 + tx + 16 * j, lq, lk);
-            const float p = on ? expf(s[i][j] * a.scale - lse_s[r]) : 0.f;
-            if (Ps) Ps[r * kLdP + tx + 16 * j] = p;
-            Ss[r * kLdP + tx + 16 * j] = on ? p * (dp[i][j] - delta_s[r]) : 0.f;
+        for (int j = 0; j < 2; ++j) y[j] = *reinterpret_cast<const float4 *>(b + 16 * j * ld + d);
+#pragma unroll
+        for (int i = 0; i < RI; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+    }
+}
+
+// acc[i][c] += sum_m w[16 i][m] b[m][64 c ..]
+template <int RI, int NC>
+__device__ __forceinline__ void add_rows(float (&acc)[RI][NC][4], const float *w, const float *b, int ldb) {
+#pragma unroll 2
+    for (int m = 0; m < kMov; m += 4) {
+        float4 x[RI];
+#pragma unroll
+        for (int i = 0; i < RI; ++i) x[i] = *reinterpret_cast<const float4 *>(w + 16 * i * kLdW + m);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const float4 y = *reinterpret_cast<const float4 *>(b + (m + u) * ldb + 64 * c);
+#pragma unroll
+                for (int i = 0; i < RI; ++i) {
+                    const float p = u == 0 ? x[i].x : u == 1 ? x[i].y : u == 2 ? x[i].z : x[i].w;
+                    acc[i][c][0] = fmaf(p, y.x, acc[i][c][0]);
+                    acc[i][c][1] = fmaf(p, y.y, acc[i][c][1]);
+                    acc[i][c][2] = fmaf(p, y.z, acc[i][c][2]);
+                    acc[i][c][3] = fmaf(p, y.w, acc[i][c][3]);
+                }
+            }
+    }
+}
+
+constexpr size_t grad_smem(int ND, int NDV, int RI, bool keys) {
+    return sizeof(float) * ((16 * RI + 2 * kMov) * (64 * ND + 4 + 64 * NDV + 4) + (keys ? 2 : 1) * 16 * RI * kLdW +
+                            (keys ? 4 * kMov : 32 * RI));
+}
+
+template <int ND, int NDV, int RI, bool KEYS>
+__global__ void __launch_bounds__(kThreads) latent_grad_f32_kernel(LatentArgs a) {
+    extern __shared__ __align__(16) float smem[];
+    constexpr int OWN = 16 * RI, D = 64 * ND, ld = D + 4, Dv = 64 * NDV, ldv = Dv + 4;
+    float *A1 = smem, *A2 = A1 + OWN * ld, *B1 = A2 + OWN * ldv, *B2 = B1 + 2 * kMov * ld, *W1 = B2 + 2 * kMov * ldv,
+          *W2 = W1 + OWN * kLdW, *stat = W2 + (KEYS ? OWN * kLdW : 0);      // lse, delta: of the rows walked over, or my own
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tx = (warp & 1) * 8 + (lane & 7), ty = (warp >> 1) * 4 + (lane >> 3), h = blockIdx.y;
+    int t;
+    // the first keys are seen by the most queries, the last queries see the most keys
+    const int n = KEYS ? find_tile(a.cu_k, a.num_seqs, a.total_k, OWN, (int)blockIdx.x, &t)
+                       : find_tile(a.cu_q, a.num_seqs, a.total_q, OWN, (int)(gridDim.x - 1 - blockIdx.x), &t);
+    const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
+    const SeqSpan own = KEYS ? sk : sq, mov = KEYS ? sq : sk;
+    const int o0 = t * OWN, count = min(OWN, own.len - o0), more = sk.len - sq.len;
+    if (count <= 0) return;
+    const int lo = KEYS && a.causal ? max(0, o0 - more) / kMov * kMov : 0;
+    const int hi = KEYS || !a.causal ? mov.len : min(mov.len, o0 + count + more);
+    const float *q = (const float *)a.q, *qs = (const float *)a.q_shared, *k = (const float *)a.k, *ks = (const float *)a.k_shared;
+    copy_rows<OWN, kThreads>(A1, ld, KEYS ? k : q, a.Dk, KEYS ? ks : qs, a.Ds, KEYS ? 1 : a.H, own.start + o0, count, a.H, h);
+    copy_rows<OWN, kThreads>(A2, ldv, (const float *)(KEYS ? a.v : a.d_out), Dv, (const float *)nullptr, 0, 1, own.start + o0,
+                             count, a.H, h);
+    auto copy = [&](int m0) {
+        const int c = min(kMov, mov.len - m0), buf = (m0 / kMov) & 1;
+        copy_rows<kMov, kThreads>(B1 + buf * kMov * ld, ld, KEYS ? q : k, a.Dk, KEYS ? qs : ks, a.Ds, KEYS ? a.H : 1,
+                                  mov.start + m0, c, a.H, h);
+        copy_rows<kMov, kThreads>(B2 + buf * kMov * ldv, ldv, (const float *)(KEYS ? a.d_out : a.v), Dv, (const float *)nullptr,
+                                  0, 1, mov.start + m0, c, a.H, h);
+        if (KEYS && tid < 2 * kMov) {
+            const int r = tid % kMov;
+            const size_t at = (size_t)(mov.start + m0 + r) * a.H + h;
+            stat[buf * 2 * kMov + tid] = r < c ? (tid < kMov ? a.lse : a.delta)[at] : 0.f;
         }
+    };
+    if (!KEYS && tid < 2 * OWN) {
+        const int r = tid % OWN;
+        const size_t at = (size_t)(own.start + o0 + r) * a.H + h;
+        stat[tid] = r < count ? (tid < OWN ? a.lse : a.delta)[at] : 0.f;
     }
-}
-
-__device__ __forceinline__ void load_stats(const LatentArgs &a, float *lse_s, float *delta_s, long row0, int rows, int h) {
-    if (threadIdx.x < kTile) {
-        const int r = threadIdx.x;
-        const size_t at = (size_t)(row0 + r) * a.H + h;
-        lse_s[r] = r < rows ? a.lse[at] : 0.f;
-        delta_s[r] = r < rows ? a.delta[at] : 0.f;
+    if (lo < hi) copy(lo);
+    cp_async_commit();
+    float acc1[RI][ND][4] = {}, acc2[RI][NDV][4] = {};
+    for (int m0 = lo; m0 < hi; m0 += kMov) {
+        const int buf = (m0 / kMov) & 1;
+        const float *b1 = B1 + buf * kMov * ld, *b2 = B2 + buf * kMov * ldv, *st = stat + (KEYS ? buf * 2 * kMov : 0);
+        cp_async_wait_all();
+        __syncthreads();                              // these rows are here, the last ones used up
+        if (m0 + kMov < hi) copy(m0 + kMov);
+        cp_async_commit();
+        float s[RI][2] = {}, dp[RI][2] = {};
+        dot_rows<RI>(s, A1 + ty * ld, b1 + tx * ld, ld, D);
+        dot_rows<RI>(dp, A2 + ty * ldv, b2 + tx * ldv, ldv, Dv);
+#pragma unroll
+        for (int i = 0; i < RI; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int o = ty + 16 * i, m = tx + 16 * j;
+                const bool on = KEYS ? seen(a, m0 + m, o0 + o, sq.len, sk.len) : seen(a, o0 + o, m0 + m, sq.len, sk.len);
+                const float lse = KEYS ? st[m] : st[o], delta = KEYS ? st[kMov + m] : st[OWN + o];
+                const float p = on ? expf(s[i][j] * a.scale - lse) : 0.f;
+                if (KEYS) W2[o * kLdW + m] = p;
+                W1[o * kLdW + m] = on ? p * (dp[i][j] - delta) : 0.f;
+            }
+        __syncthreads();
+        add_rows<RI, ND>(acc1, W1 + ty * kLdW, b1 + 4 * tx, ld);
+        if (KEYS) add_rows<RI, NDV>(acc2, W2 + ty * kLdW, b2 + 4 * tx, ldv);
     }
-}
-
-template <typename T, int ND, int NDV>
-__global__ void __launch_bounds__(kThreads) latent_dkv_f32_kernel(LatentArgs a) {
-    extern __shared__ __align__(16) float smem[];
-    constexpr int D = 64 * ND, ld = D + 4, Dv = 64 * NDV, ldv = Dv + 4;
-    float *Ks = smem, *Vs = Ks + kTile * ld, *Qs = Vs + kTile * ldv, *Os = Qs + kTile * ld, *Ps = Os + kTile * ldv,
-          *Ss = Ps + kTile * kLdP, *lse_s = Ss + kTile * kLdP, *delta_s = lse_s + kTile;
-    int t;
-    const int n = find_tile(a.cu_k, a.num_seqs, a.total_k, kTile, (int)blockIdx.x, &t);
-    const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
-    const int h = blockIdx.y, k0 = t * kTile;
-    const int keys = min(kTile, sk.len - k0);
-    if (keys <= 0) return;
-    load_rows<T>(Ks, ld, (const T *)a.k, a.Dk, (const T *)a.k_shared, a.Ds, 1, sk.start + k0, keys, a.H, h);
-    load_rows<T>(Vs, ldv, (const T *)a.v, Dv, (const T *)nullptr, 0, 1, sk.start + k0, keys, a.H, h);
-    float dk[4][ND][4] = {}, dv[4][NDV][4] = {};
-    // the first row that sees key k0
-    const int first = a.causal ? max(0, k0 - (sk.len - sq.len)) : 0;
-    for (int r0 = first / kTile * kTile; r0 < sq.len; r0 += kTile) {
-        const int rows = min(kTile, sq.len - r0);
-        __syncthreads();
-        load_rows<T>(Qs, ld, (const T *)a.q, a.Dk, (const T *)a.q_shared, a.Ds, a.H, sq.start + r0, rows, a.H, h);
-        load_rows<T>(Os, ldv, (const T *)a.d_out, Dv, (const T *)nullptr, 0, 1, sq.start + r0, rows, a.H, h);
-        load_stats(a, lse_s, delta_s, sq.start + r0, rows, h);
-        __syncthreads();
-        tile_grads(a, Qs, Ks, ld, D, Os, Vs, ldv, Dv, lse_s, delta_s, r0, k0, sq.len, sk.len, Ps, Ss);
-        __syncthreads();
-        cols_times<NDV>(dv, Ps, Os, ldv);
-        cols_times<ND>(dk, Ss, Qs, ld);
+    cp_async_wait_all();                              // nothing lands after the CTA has left
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+        if (ty + 16 * i >= count) continue;
+        const size_t row = (size_t)(own.start + o0 + ty + 16 * i) * a.H + h;
+#pragma unroll
+        for (int c = 0; c < ND; ++c) {
+            const int col = 64 * c + 4 * tx;
+            const float f = a.scale, *x = acc1[i][c];
+            float *to = col < a.Dk ? (float *)(KEYS ? a.dk : a.dq) + row * a.Dk + col
+                                   : (KEYS ? a.dks_heads : (float *)a.dq_shared) + row * a.Ds + (col - a.Dk);
+            *reinterpret_cast<float4 *>(to) = make_float4(f * x[0], f * x[1], f * x[2], f * x[3]);
+        }
+        if (KEYS)
+#pragma unroll
+            for (int c = 0; c < NDV; ++c) {
+                const float *x = acc2[i][c];
+                *reinterpret_cast<float4 *>((float *)a.dv + row * Dv + 64 * c + 4 * tx) = make_float4(x[0], x[1], x[2], x[3]);
+            }
     }
-    store_rows<T, T, 4, NDV>(dv, 1.f, (T *)a.dv, Dv, (T *)nullptr, 0, sk.start + k0, keys, a.H, h);
-    store_rows<T, float, 4, ND>(dk, a.scale, (T *)a.dk, a.Dk, a.dks_heads, a.Ds, sk.start + k0, keys, a.H, h);
-}
-
-template <typename T, int ND, int NDV>
-__global__ void __launch_bounds__(kThreads) latent_dq_f32_kernel(LatentArgs a) {
-    extern __shared__ __align__(16) float smem[];
-    constexpr int D = 64 * ND, ld = D + 4, Dv = 64 * NDV, ldv = Dv + 4;
-    float *Ks = smem, *Vs = Ks + kTile * ld, *Qs = Vs + kTile * ldv, *Os = Qs + kTile * ld, *Ss = Os + kTile * ldv,
-          *lse_s = Ss + kTile * kLdP, *delta_s = lse_s + kTile;
-    int t;
-    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, kTile, (int)(gridDim.x - 1 - blockIdx.x), &t);
-    const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
-    const int h = blockIdx.y, r0 = t * kTile;
-    const int rows = min(kTile, sq.len - r0);
-    if (rows <= 0) return;
-    load_rows<T>(Qs, ld, (const T *)a.q, a.Dk, (const T *)a.q_shared, a.Ds, a.H, sq.start + r0, rows, a.H, h);
-    load_rows<T>(Os, ldv, (const T *)a.d_out, Dv, (const T *)nullptr, 0, 1, sq.start + r0, rows, a.H, h);
-    load_stats(a, lse_s, delta_s, sq.start + r0, rows, h);
-    float dq[4][ND][4] = {};
-    const int kend = a.causal ? min(sk.len, r0 + rows + sk.len - sq.len) : sk.len;
-    for (int k0 = 0; k0 < kend; k0 += kTile) {
-        const int keys = min(kTile, sk.len - k0);
-        __syncthreads();
-        load_rows<T>(Ks, ld, (const T *)a.k, a.Dk, (const T *)a.k_shared, a.Ds, 1, sk.start + k0, keys, a.H, h);
-        load_rows<T>(Vs, ldv, (const T *)a.v, Dv, (const T *)nullptr, 0, 1, sk.start + k0, keys, a.H, h);
-        __syncthreads();
-        tile_grads(a, Qs, Ks, ld, D, Os, Vs, ldv, Dv, lse_s, delta_s, r0, k0, sq.len, sk.len, nullptr, Ss);
-        __syncthreads();
-        rows_times<4, ND>(dq, Ss, Ks, ld);
-    }
-    store_rows<T, T, 4, ND>(dq, a.scale, (T *)a.dq, a.Dk, (T *)a.dq_shared, a.Ds, sq.start + r0, rows, a.H, h);
 }
 
 // delta_i = d_out_i . out_i: one warp per (row, head).
@@ -404,10 +435,11 @@ __global__ void __launch_bounds__(256) latent_shared_sum_kernel(const float *par
     Io<T>::st4(out + row * Ds + c, x);
 }
 
-// Fewer tiles of 64 rows than SMs: tiles of 16, and the keys split until two CTAs per SM have work (8 at most).
-bool forward_few(int total_q, int H) { return (long)(total_q / kTile + 1) * H < 148; }
+// Fewer tiles of 64 rows than SMs: smaller tiles; in the forward pass of 16, and the keys split until two CTAs per
+// SM have work (8 at most).
+bool few_tiles(int total, int H) { return (long)(total / kTile + 1) * H < 148; }
 int forward_splits(int total_q, int total_k, int H) {
-    if (!forward_few(total_q, H)) return 1;
+    if (!few_tiles(total_q, H)) return 1;
     const long ctas = (long)(total_q / 16 + 1) * H, want = 296 / ctas, tiles = (total_k + kTile - 1) / kTile;
     return (int)std::max(1L, std::min({want, tiles, 8L}));
 }
@@ -432,32 +464,26 @@ template <typename T, int NDV, int RI, int NT> cudaError_t forward_ri(const Late
     return cudaGetLastError();
 }
 template <typename T, int NDV> cudaError_t forward_nv(const LatentArgs &a, cudaStream_t s) {
-    if (!forward_few(a.total_q, a.H)) return forward_ri<T, NDV, 4, 512>(a, 1, s);
+    if (!few_tiles(a.total_q, a.H)) return forward_ri<T, NDV, 4, 512>(a, 1, s);
     return forward_ri<T, NDV, 1, 256>(a, forward_splits(a.total_q, a.total_k, a.H), s);
 }
 
-template <typename T, int ND, int NDV> cudaError_t backward_nd(const LatentArgs &a, cudaStream_t s) {
-    constexpr size_t tiles = 2 * (64 * ND + 4) + 2 * (64 * NDV + 4);
-    constexpr size_t bkv = sizeof(float) * kTile * (tiles + 2 * kLdP + 2), bq = sizeof(float) * kTile * (tiles + kLdP + 2);
-    cudaError_t e = allow_smem<latent_dkv_f32_kernel<T, ND, NDV>>(bkv);
-    if (e == cudaSuccess) e = allow_smem<latent_dq_f32_kernel<T, ND, NDV>>(bq);
+template <int ND, int NDV, int RI, bool KEYS> cudaError_t grad_ri(const LatentArgs &a, cudaStream_t s) {
+    constexpr size_t bytes = grad_smem(ND, NDV, RI, KEYS);
+    const cudaError_t e = allow_smem<latent_grad_f32_kernel<ND, NDV, RI, KEYS>>(bytes);
     if (e != cudaSuccess) return e;
-    if (a.total_k > 0) {
-        const dim3 grid(tile_slots(a.total_k, a.num_seqs, kTile), a.H);
-        latent_dkv_f32_kernel<T, ND, NDV><<<grid, kThreads, bkv, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (a.total_q > 0) {
-        const dim3 grid(tile_slots(a.total_q, a.num_seqs, kTile), a.H);
-        latent_dq_f32_kernel<T, ND, NDV><<<grid, kThreads, bq, s>>>(a);
-    }
+    const dim3 grid(tile_slots(KEYS ? a.total_k : a.total_q, a.num_seqs, 16 * RI), a.H);
+    latent_grad_f32_kernel<ND, NDV, RI, KEYS><<<grid, kThreads, bytes, s>>>(a);
     return cudaGetLastError();
 }
-template <typename T> cudaError_t backward_t(const LatentArgs &a, cudaStream_t s) {
-    const int nd = (a.Dk + a.Ds) / 64;
-    if (a.Dv == 64)
-        return nd == 1 ? backward_nd<T, 1, 1>(a, s) : nd == 2 ? backward_nd<T, 2, 1>(a, s) : backward_nd<T, 3, 1>(a, s);
-    return nd == 1 ? backward_nd<T, 1, 2>(a, s) : nd == 2 ? backward_nd<T, 2, 2>(a, s) : backward_nd<T, 3, 2>(a, s);
+template <int ND, int NDV, bool KEYS> cudaError_t grad(const LatentArgs &a, cudaStream_t s) {
+    const int total = KEYS ? a.total_k : a.total_q;
+    if (total == 0) return cudaSuccess;
+    return few_tiles(total, a.H) ? grad_ri<ND, NDV, 2, KEYS>(a, s) : grad_ri<ND, NDV, 4, KEYS>(a, s);
+}
+template <int ND, int NDV> cudaError_t backward_nd(const LatentArgs &a, cudaStream_t s) {
+    const cudaError_t e = grad<ND, NDV, true>(a, s);
+    return e == cudaSuccess ? grad<ND, NDV, false>(a, s) : e;
 }
 
 // ---------------------------------------------------------------------------
@@ -718,7 +744,9 @@ cudaError_t launch_latent_shared_sum(const LatentArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_latent_backward_f32(const LatentArgs &a, cudaStream_t s) {
-    return backward_t<float>(a, s);
+    const int nd = (a.Dk + a.Ds) / 64;
+    if (a.Dv == 64) return nd == 1 ? backward_nd<1, 1>(a, s) : nd == 2 ? backward_nd<2, 1>(a, s) : backward_nd<3, 1>(a, s);
+    return nd == 1 ? backward_nd<1, 2>(a, s) : nd == 2 ? backward_nd<2, 2>(a, s) : backward_nd<3, 2>(a, s);
 }
 
 cudaError_t launch_latent_decode_f32(const LatentDecodeArgs &a, cudaStream_t s) {
