@@ -154,9 +154,9 @@ __global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a, in
     float *Qs = smem, *Ps = Qs + M * ld, *KV = Ps + M * kLdP;
     int t;
     // the last tiles of a sequence see the most keys: start with them
-    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, M, (int)(gridDim.x - 1 - blockIdx.x), &t);
+    const int n = find_tile(a.cu_q, a.num_seqs, a.total_q, M, (int)((gridDim.x - 1 - blockIdx.x) / a.H), &t);
     const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
-    const int h = blockIdx.y, r0 = t * M;
+    const int h = blockIdx.x % a.H, r0 = t * M;
     const int rows = min(M, sq.len - r0);
     if (rows <= 0) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -317,11 +317,12 @@ __global__ void __launch_bounds__(kThreads) latent_grad_f32_kernel(LatentArgs a)
     float *A1 = smem, *A2 = A1 + OWN * ld, *B1 = A2 + OWN * ldv, *B2 = B1 + 2 * kMov * ld, *W1 = B2 + 2 * kMov * ldv,
           *W2 = W1 + OWN * kLdW, *stat = W2 + (KEYS ? OWN * kLdW : 0);      // lse, delta: of the rows walked over, or my own
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tx = (warp & 1) * 8 + (lane & 7), ty = (warp >> 1) * 4 + (lane >> 3), h = blockIdx.y;
+    const int tx = (warp & 1) * 8 + (lane & 7), ty = (warp >> 1) * 4 + (lane >> 3);
+    const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H, slots = gridDim.x / a.H;
     int t;
     // the first keys are seen by the most queries, the last queries see the most keys
-    const int n = KEYS ? find_tile(a.cu_k, a.num_seqs, a.total_k, OWN, (int)blockIdx.x, &t)
-                       : find_tile(a.cu_q, a.num_seqs, a.total_q, OWN, (int)(gridDim.x - 1 - blockIdx.x), &t);
+    const int n = KEYS ? find_tile(a.cu_k, a.num_seqs, a.total_k, OWN, slot, &t)
+                       : find_tile(a.cu_q, a.num_seqs, a.total_q, OWN, slots - 1 - slot, &t);
     const SeqSpan sq = seq_span(a.cu_q, n, a.total_q), sk = seq_span(a.cu_k, n, a.total_k);
     const SeqSpan own = KEYS ? sk : sq, mov = KEYS ? sq : sk;
     const int o0 = t * OWN, count = min(OWN, own.len - o0), more = sk.len - sq.len;
@@ -454,7 +455,7 @@ template <typename T, int NDV, int RI, int NT> cudaError_t forward_ri(const Late
     if (e != cudaSuccess) return e;
     const int ld = a.Dk + a.Ds + 4;
     const size_t bytes = sizeof(float) * (M * (ld + kLdP) + BUF * kTile * (ld + (64 * NDV + 4)));
-    const dim3 grid(tile_slots(a.total_q, a.num_seqs, M), a.H, splits);
+    const dim3 grid(tile_slots(a.total_q, a.num_seqs, M) * a.H, 1, splits);
     latent_forward_f32_kernel<T, NDV, RI, NT><<<grid, NT, bytes, s>>>(a, splits);
     if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
     LatentDecodeArgs j{};
@@ -472,7 +473,7 @@ template <int ND, int NDV, int RI, bool KEYS> cudaError_t grad_ri(const LatentAr
     constexpr size_t bytes = grad_smem(ND, NDV, RI, KEYS);
     const cudaError_t e = allow_smem<latent_grad_f32_kernel<ND, NDV, RI, KEYS>>(bytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid(tile_slots(KEYS ? a.total_k : a.total_q, a.num_seqs, 16 * RI), a.H);
+    const int grid = tile_slots(KEYS ? a.total_k : a.total_q, a.num_seqs, 16 * RI) * a.H;      // heads side by side
     latent_grad_f32_kernel<ND, NDV, RI, KEYS><<<grid, kThreads, bytes, s>>>(a);
     return cudaGetLastError();
 }
