@@ -11,9 +11,9 @@
 // consecutive rows on different banks).  Bound by the FMA pipes and the reads of
 // shared memory that feed them.
 //
-// Measured: 16 heads of 128 + 64 and 128, T = 1100, causal: 393 us, 15.8 TFLOP/s;
-// two heads, T = 256: 7.9 us and 3.9 us for the join (22.5 us without the split of the
-// keys).
+// Measured, 16 heads of 128 + 64 and 128, causal: T = 1100 in 247 us, T = 2000 in 678
+// us (25 and 30 TFLOP/s), gradients of T = 900 in 621 us (17); two heads, T = 256: 7.9
+// us and 3.9 us for the join.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -138,8 +138,8 @@ __device__ __forceinline__ bool seen(const LatentArgs &a, int i, int j, int lq, 
 
 // ---------------------------------------------------------------------------
 // Forward: one CTA per (RI NT / 16 query rows, head), online softmax over key
-// tiles.  RI = 4 with 512 threads (128 rows) reads each operand for four products
-// and keeps 16 warps on an SM; RI = 1 with 256 threads (16 rows) makes eight times
+// tiles.  RI = 4 with 512 threads (128 rows) or 256 (64) reads each operand for four
+// products; RI = 1 with 256 threads (16 rows) makes eight times
 // as many CTAs, for calls that would leave SMs empty, copies the next key tile
 // while it works on one, and may split the keys over `splits` CTAs (blockIdx.z),
 // whose results a second kernel joins.  Two heads of 256 queries: 22.5 us with 16
@@ -258,7 +258,9 @@ __global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a, in
 // 4 x 8 lanes a warp: with RI = 4 a thread's products over four columns read six
 // 128-byte rows of shared memory for 32 FMAs a lane, its sums 16 for 192.  RI = 2
 // makes twice the CTAs, where 64 rows each would leave SMs empty.
-// Measured (16 heads of 128 + 64 and 128, T = 900, causal): @@
+// Measured (16 heads of 128 + 64 and 128, T = 900, causal): 621 us for both sides, 899
+// with a head's tiles side by side instead of the heads (an SM idle for half the
+// time), 997 without the copies meanwhile and with 2 x 16 lanes a warp.
 // ---------------------------------------------------------------------------
 constexpr int kMov = 32, kLdW = 40;
 
@@ -465,7 +467,10 @@ template <typename T, int NDV, int RI, int NT> cudaError_t forward_ri(const Late
     return cudaGetLastError();
 }
 template <typename T, int NDV> cudaError_t forward_nv(const LatentArgs &a, cudaStream_t s) {
-    if (!few_tiles(a.total_q, a.H)) return forward_ri<T, NDV, 4, 512>(a, 1, s);
+    // 128 rows a CTA, unless 64 balance better: up to one and a half waves of them (16 heads of 1100 queries: 247 us
+    // with 64 rows, 385 with 128; of 1500: 445 and 510; of 2000: 735 and 678).
+    if (!few_tiles(a.total_q, a.H))
+        return (long)(a.total_q / 128 + 1) * a.H < 222 ? forward_ri<T, NDV, 4, 256>(a, 1, s) : forward_ri<T, NDV, 4, 512>(a, 1, s);
     return forward_ri<T, NDV, 1, 256>(a, forward_splits(a.total_q, a.total_k, a.H), s);
 }
 
