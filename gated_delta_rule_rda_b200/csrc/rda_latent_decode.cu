@@ -115,10 +115,12 @@ __host__ __device__ inline uint32_t operand_bytes(int nt, int D, int pairs, int 
 }
 
 // Partial results: [group][row tile][first or last segment][column] -> Dl floats,
-// then their log-sum-exps, then what each group leaves unfinished.
+// then their log-sum-exps, then the sequences that are left in parts: a record per
+// sequence where there are no more of them than groups, per group otherwise (a
+// group leaves one at most).
 struct Parts {
     float *o, *lse;
-    int4 *rec;                           // {sequence or -1, last group, slot of the first part, -}
+    int4 *rec;                           // {sequence or -1, last group, slot of the first part, first group}
 };
 __host__ __device__ inline size_t part_slots(const Geometry &g) { return (size_t)g.groups * g.rt * 2; }
 __host__ __device__ inline Parts parts_of(float *base, const Geometry &g, int Dl) {
@@ -386,8 +388,9 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
         tc_fence_before();
         mbar_arrive(&S.o_empty);
         named_bar_sync(bar, 128);                                  // factors are free again
-        if (rt == 0 && threadIdx.x == 32 * kSoftWarp && walk.pos >= hi) {
-            // this group's last segment: does its sequence begin here and go on in others?
+        const bool by_seq = a.B <= g.groups;
+        if (rt == 0 && threadIdx.x == 32 * kSoftWarp && (by_seq ? walk.t0 == 0 : walk.pos >= hi)) {
+            // does a sequence begin here and go on in other groups?
             int4 rec = make_int4(-1, 0, 0, 0);
             if (!done && walk.t0 == 0) {
                 const long long groups = min((long long)g.groups, total);
@@ -395,9 +398,9 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
                 long long gl = min(groups - 1, end * groups / total);     // the group that holds it
                 while (gl + 1 < groups && total * (gl + 1) / groups <= end) ++gl;
                 while (total * gl / groups > end) --gl;
-                rec = make_int4(walk.seq, (int)gl, first_segment ? 0 : 1, 0);
+                rec = make_int4(walk.seq, (int)gl, first_segment ? 0 : 1, grp);
             }
-            parts.rec[grp] = rec;
+            parts.rec[by_seq ? walk.seq : grp] = rec;
         }
         first_segment = false;
     }
@@ -706,7 +709,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
         const SoftmaxCtx<NT> x{S, args, walk, w, p_s, tmem, rt, grp, rows, row0, hi, total};
         if (warp < kSoftWarp + 4) softmax<NT, split_cols(NT)>(x, 0);
         else if constexpr (NT > 16) softmax<NT, NT - split_cols(NT)>(x, 1);
-        if (rt == 0 && tid == 32 * kSoftWarp && lo >= hi) parts_of(a.part, g, a.Dl).rec[grp] = make_int4(-1, 0, 0, 0);
+        if (rt == 0 && tid == 32 * kSoftWarp && lo >= hi && a.B > g.groups) parts_of(a.part, g, a.Dl).rec[grp] = make_int4(-1, 0, 0, 0);
     }
     tc_fence_before();
     __syncthreads();
@@ -716,63 +719,84 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
     }
 }
 
-// Joins the parts of the sequence that begins in group blockIdx.x and goes on in
-// others: out = sum_i e^{lse_i - lse} o_i.  128 threads per row and share of the
-// parts: SHARES = 4 takes a row per CTA, each quarter of it every fourth part;
-// SHARES = 1 takes four rows per CTA.  The parts come from L2: 3 to 6 us.
-constexpr int kJoin = 512;
-template <int SHARES> __global__ void __launch_bounds__(kJoin) latent_join_bf16_kernel(const Args args) {
-    __shared__ float4 acc_s[SHARES][128];
+// Joins the parts of the sequence of record blockIdx.x: out = sum_i e^{lse_i - lse} o_i.
+// MANY: a CTA per row and 128 columns, each of its 16 warps takes every 16th part;
+// otherwise four rows a CTA, 128 threads each.  The parts come from L2; what counts
+// is how few loads wait for one another: the record, then log-sum-exps and the
+// first parts at once.
+constexpr int kJoin = 512, kMostParts = 160;
+static_assert(kMostParts >= kCtas && kMostParts % 32 == 0, "parts of a sequence");
+template <bool MANY> __global__ void __launch_bounds__(kJoin) latent_join_bf16_kernel(const Args args) {
+    constexpr int SHARES = MANY ? kJoin / 32 : 1;
+    __shared__ float4 acc_s[SHARES][32];
+    __shared__ float w_s[kJoin / 32][kMostParts];
     const LatentDecodeArgs &a = args.a;
     const Geometry &g = args.g;
     const Parts parts = parts_of(a.part, g, a.Dl);
-    const int tid = threadIdx.x, lane = tid & 31, group = tid >> 7, c = (tid & 127) * 4;
-    const int share = SHARES == 4 ? group : 0;
-    const int grp = blockIdx.x, at = SHARES == 4 ? blockIdx.y : blockIdx.y * 4 + group;     // row, by tile
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int share = MANY ? warp : 0, c = MANY ? blockIdx.z * 128 + lane * 4 : (tid & 127) * 4;
+    const int at = MANY ? blockIdx.y : blockIdx.y * 4 + (tid >> 7);       // row, by tile
     const int rt = at / g.rows, r = at % g.rows, R = a.T * a.H;
     const bool on = at < g.rt * g.rows && rt * g.rows + r < R;
     pdl_launch_dependents();
     pdl_wait_primary();
-    const int4 rec = parts.rec[grp];
+    const int4 rec = parts.rec[blockIdx.x];
     if (rec.x < 0 || !on) return;
-    const int n = rec.y - grp + 1;
-    auto slot = [&](int i) { return (((size_t)(grp + i) * g.rt + rt) * 2 + (i == 0 ? rec.z : 0)) * g.nt + r; };
+    const int n = rec.y - rec.w + 1;
+    auto slot = [&](int i) { return (((size_t)(rec.w + i) * g.rt + rt) * 2 + (i == 0 ? rec.z : 0)) * g.nt + r; };
+    auto part = [&](int i) {
+        return i < n && c < a.Dl ? *reinterpret_cast<const float4 *>(parts.o + slot(i) * a.Dl + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) y[u] = part(share + u * SHARES);
+    float l[kMostParts / 32], top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kMostParts / 32; ++j) {
+        l[j] = 32 * j + lane < n ? parts.lse[slot(32 * j + lane)] : -INFINITY;
+        top = fmaxf(top, l[j]);
+    }
     // every warp computes the common maximum and sum
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, parts.lse[slot(i)]);
 #pragma unroll
     for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    for (int i = lane; i < n; i += 32) sum += expf(parts.lse[slot(i)] - base);
+#pragma unroll
+    for (int j = 0; j < kMostParts / 32; ++j) {
+        l[j] = expf(l[j] - base);
+        sum += l[j];
+    }
 #pragma unroll
     for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     const float f = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int j = 0; j < kMostParts / 32; ++j) w_s[warp][32 * j + lane] = l[j] * f;
+    __syncwarp();
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < a.Dl) {
-#pragma unroll 4
-        for (int i = share; i < n; i += SHARES) {
-            const size_t s = slot(i);
-            const float4 y = *reinterpret_cast<const float4 *>(parts.o + s * a.Dl + c);
-            const float wi = expf(parts.lse[s] - base) * f;
-            x.x = fmaf(wi, y.x, x.x), x.y = fmaf(wi, y.y, x.y), x.z = fmaf(wi, y.z, x.z), x.w = fmaf(wi, y.w, x.w);
+    for (int i = share; i < n; i += 4 * SHARES) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = i + u * SHARES;
+            const float w = k < n ? w_s[warp][k] : 0.f;
+            x.x = fmaf(w, y[u].x, x.x), x.y = fmaf(w, y[u].y, x.y), x.z = fmaf(w, y[u].z, x.z), x.w = fmaf(w, y[u].w, x.w);
+            y[u] = part(k + 4 * SHARES);
         }
     }
-    if (SHARES == 4) {
-        acc_s[share][tid & 127] = x;
+    if (MANY) {
+        acc_s[share][lane] = x;
         __syncthreads();
         if (share) return;
 #pragma unroll
-        for (int i = 1; i < 4; ++i) {
-            const float4 y = acc_s[i % SHARES][tid];
-            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        for (int i = 1; i < SHARES; ++i) {
+            const float4 z = acc_s[i][lane];
+            x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
         }
     }
     const size_t row = (size_t)rec.x * R + rt * g.rows + r;
     if (c < a.Dl)
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * a.Dl + c) =
             make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
-    if ((tid & 127) == 0 && a.lse) a.lse[row] = sum > 0.f ? base + logf(sum) : -INFINITY;
+    if (c == 0 && a.lse) a.lse[row] = sum > 0.f ? base + logf(sum) : -INFINITY;
 }
 
 template <int NT> uint32_t small_bytes() { return (uint32_t)sizeof(Small<NT>); }
@@ -833,11 +857,11 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s) {
         default: e = launch<64>(maps, args, s); break;
     }
     if (e != cudaSuccess || args.g.groups == 1) return e;
-    // Parts per sequence: about groups / B.  From 16 on a whole CTA per row pays (the parts are read in turn).
+    // Parts per sequence: about groups / B.  From 16 on many warps share a row (@@).
     const bool many = args.g.groups >= 16 * a.B;
-    const int at = args.g.rt * args.g.rows;
-    const dim3 grid(args.g.groups, many ? at : (at + 3) / 4);
-    return launch_after(many ? latent_join_bf16_kernel<4> : latent_join_bf16_kernel<1>, grid, kJoin, 0, s, args);
+    const int at = args.g.rt * args.g.rows, records = std::min(a.B, args.g.groups);
+    return many ? launch_after(latent_join_bf16_kernel<true>, dim3(records, at, a.Dl / 128), kJoin, 0, s, args)
+                : launch_after(latent_join_bf16_kernel<false>, dim3(records, (at + 3) / 4), kJoin, 0, s, args);
 }
 
 }  // namespace rda
