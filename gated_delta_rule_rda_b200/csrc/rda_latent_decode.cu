@@ -39,7 +39,7 @@
 // P is rounded to bf16 for its product (its scale is that of the running
 // maximum, its relative error 2^-8 at most); sums and statistics are fp32.
 //
-// Measured (Dl + Ds = 512 + 64, 16 heads; this kernel, without the join's 5 to 8 us):
+// Measured (Dl + Ds = 512 + 64, 16 heads; this kernel, without the join):
 //   256 sequences of up to 4096 tokens, 16 rows     106 us, 5.8 TB/s (88% of a copy's rate)
 //   32 of up to 8192, 8 tokens: 128 rows, two CTAs   78 us; what bounds it is how long a
 //               tile stays in the ring, which holds two beside 64 rows of Q: 3,300 cycles a
@@ -723,7 +723,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
 // MANY: a CTA per row and 128 columns, each of its 16 warps takes every 16th part;
 // otherwise four rows a CTA, 128 threads each.  The parts come from L2; what counts
 // is how few loads wait for one another: the record, then log-sum-exps and the
-// first parts at once.
+// first parts at once.  4 us for one sequence of 16 rows, 8 for 256, 13 for 32 of 128
+// rows (28 MB of parts); rows walked over in one wave of CTAs were no faster.
 constexpr int kJoin = 512, kMostParts = 160;
 static_assert(kMostParts >= kCtas && kMostParts % 32 == 0, "parts of a sequence");
 template <bool MANY> __global__ void __launch_bounds__(kJoin) latent_join_bf16_kernel(const Args args) {
@@ -857,7 +858,8 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t s) {
         default: e = launch<64>(maps, args, s); break;
     }
     if (e != cudaSuccess || args.g.groups == 1) return e;
-    // Parts per sequence: about groups / B.  From 16 on many warps share a row (@@).
+    // Parts per sequence: about groups / B.  From 16 on 16 warps share a row: 64 parts of 16 rows take 3.8 us so,
+    // 13.3 with four warps a row.
     const bool many = args.g.groups >= 16 * a.B;
     const int at = args.g.rt * args.g.rows, records = std::min(a.B, args.g.groups);
     return many ? launch_after(latent_join_bf16_kernel<true>, dim3(records, at, a.Dl / 128), kJoin, 0, s, args)
