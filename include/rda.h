@@ -430,6 +430,8 @@ rda_status_t rda_prefill_chunked_noalloc(const void *q, const void *k, const voi
  *   Dk, Dv in {64, 128}, Ds in {0, 64}, H <= 1024; total * H * (Dk + Ds) and
  *                  (total + num_seqs) * H below 2^31
  * A device-side wait that runs out records RDA_ERR_TIMEOUT as in the prefill calls.
+ * Here and below a workspace serves one call at a time: calls, or graphs, that may
+ * run at once need one each; those that follow one another on a stream may share it.
  * Preconditions, not checked: finite inputs within the sequences.  Sums, softmax
  * statistics and (for fp32) products are fp32; bf16 inputs run on the tensor cores,
  * with the probabilities rounded to bf16 for their product with v.
