@@ -603,7 +603,7 @@ def rda_latent_decode(q, pages, block_table, seq_lens, *, scale, q_shared=None, 
         _need_like(lse, "lse", (B, T, H), torch.float32, dev)
     with _allocating_on(stream):
         if out is None:
-            out = q.new_empty((B, T, H, Dl))
+            out = torch.empty_like(q)
         if lse is None and return_lse:
             lse = q.new_empty((B, T, H), dtype=torch.float32)
         if workspace is None:
@@ -640,7 +640,7 @@ def rda_verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, nu
         _need_like(num_accepted, "num_accepted", (B,), torch.int32, dev)
     with _allocating_on(stream):
         if tokens is None:
-            tokens = draft_tokens.new_empty((B, T + 1))
+            tokens = torch.empty_like(uniforms, dtype=torch.int32)
         if num_accepted is None:
             num_accepted = draft_tokens.new_empty((B,))
         if workspace is None:

@@ -116,19 +116,27 @@ size_t order_bytes(int total, int num_seqs, int tile);
 // whatever comes next finds both done; it lets its own dependents go at once.
 // Measured in calls one after the other: 22.6 -> 19.2 us for one sequence of
 // 4096 tokens decoded, 71.5 -> 64.6 us for the gradients of a packed batch.
+// `cluster` CTAs along x form a cluster.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A &&...args) {
+cudaError_t launch_clusters_after(void (*kernel)(P...), int cluster, dim3 grid, int threads, size_t smem, cudaStream_t s, A &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A &&...args) {
+    return launch_clusters_after(kernel, 1, grid, threads, smem, s, std::forward<A>(args)...);
 }
 
 cudaError_t launch_latent_forward_f32(const LatentArgs &a, cudaStream_t s);

@@ -13,14 +13,14 @@
 // differences are exact there, and a choice then hangs on the order of the sum
 // only where u lies within ~1e-14 of a border.
 //
-// Two kernels.  sums: a warp per 1024-token slice, all its loads in flight at
-// once, one fp64 sum a slice.  pick: a CTA per sequence scans the slices' sums,
-// re-reads the one slice that u falls into (from L2) and scans it.
+// Sums: a warp per 1024-token slice, all its loads in flight at once, one fp64 sum a
+// slice.  Draw: one CTA a sequence scans the slices' sums, re-reads the one slice
+// that u falls into (from L2) and scans it.  One kernel, a cluster per sequence, or
+// two (see the launch).
 // Sums run in a fixed order: results do not depend on timing.
 //
 // Measured: 64 sequences, V = 259,840: sums 22.7 us (5.9 TB/s, 89% of a copy's rate),
-// both kernels 27.2 us; one sequence, V = 32,000: 15 us, of which the host's two
-// launches are most (2.8 and 3.7 us on the device).
+// both kernels 26 us; one sequence, V = 32,000: 5.2 us, 12.7 with the host's part.
 #include <cuda_runtime.h>
 
 #include "rda_latent.h"
@@ -30,8 +30,12 @@ namespace rda {
 namespace {
 
 constexpr int kSlice = 1024;      // tokens a warp sums at once: 8 float4 of each row per lane
-constexpr int kWarps = 8;
-constexpr int kPick = 256;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMostCtas = 8;      // of a sequence (the portable size of a cluster)
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 __host__ __device__ constexpr int slices_of(int V) { return (V + kSlice - 1) / kSlice; }
 
@@ -112,22 +116,6 @@ template <bool VEC> __device__ __forceinline__ double slice_sum(const Rows &r, i
     return sum;
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(32 * kWarps) verify_sums_kernel(VerifyArgs a) {
-    const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    ptx::pdl_launch_dependents();
-    ptx::pdl_wait_primary();
-    int n;
-    const int k = kept_drafts(a, b, lane, &n);
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.num_accepted[b] = k;
-    const Rows r = weight_rows(a, b, k, n);
-    const int ns = slices_of(a.V);
-    for (int s = blockIdx.x * kWarps + warp; s < ns; s += gridDim.x * kWarps) {
-        const double sum = slice_sum<VEC>(r, s, a.V, lane);
-        if (lane == 0) a.part[(size_t)b * ns + s] = sum;
-    }
-}
-
 // Inclusive sums over the CTA's threads; *total gets the sum of all.
 __device__ __forceinline__ double block_scan(double x, double *warp_s, double *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -141,7 +129,7 @@ __device__ __forceinline__ double block_scan(double x, double *warp_s, double *t
     __syncthreads();
     double before = 0.0, sum = 0.0;
 #pragma unroll
-    for (int w = 0; w < kPick / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w == warp) before = sum;
         sum += warp_s[w];
     }
@@ -149,21 +137,16 @@ __device__ __forceinline__ double block_scan(double x, double *warp_s, double *t
     return before + x;
 }
 
-__global__ void __launch_bounds__(kPick) verify_pick_kernel(VerifyArgs a) {
-    __shared__ double warp_s[kPick / 32], start_s;
+// The token of sequence b after its k kept drafts of n, from the slices' sums: by one CTA, which saw them written.
+__device__ __forceinline__ void draw(const VerifyArgs &a, int b, int k, int n, double *part) {
+    __shared__ double warp_s[kWarps], start_s;
     __shared__ int slice_s, last_s, token_s, tail_s;
-    const int b = blockIdx.x, tid = threadIdx.x;
+    const int tid = threadIdx.x, ns = slices_of(a.V);
     if (tid == 0) slice_s = token_s = 0x7fffffff, last_s = tail_s = -1, start_s = 0.0;
-    const int ns = slices_of(a.V);
-    double *part = a.part + (size_t)b * ns;
-    ptx::pdl_launch_dependents();
-    ptx::pdl_wait_primary();
-    const int n = a.num_drafts ? min(max(a.num_drafts[b], 0), a.T) : a.T;
     const double u = a.uniforms[(size_t)b * (a.T + 1) + a.T];
-    const int k = a.num_accepted[b];
     Rows r = weight_rows(a, b, k, n);
     // each thread's slices are consecutive: one scan gives every slice's start
-    const int per = (ns + kPick - 1) / kPick, s0 = min(ns, tid * per), s1 = min(ns, s0 + per);
+    const int per = (ns + kThreads - 1) / kThreads, s0 = min(ns, tid * per), s1 = min(ns, s0 + per);
     double mine, end, total;
     for (int pass = 0;; ++pass) {
         mine = 0.0;
@@ -173,7 +156,7 @@ __global__ void __launch_bounds__(kPick) verify_pick_kernel(VerifyArgs a) {
         // a residual of nothing (the target nowhere above the draft): the target itself
         r.q = nullptr;
         r.x = -1;
-        for (int s = tid >> 5; s < ns; s += kPick / 32) {
+        for (int s = tid >> 5; s < ns; s += kThreads / 32) {
             const double sum = slice_sum<false>(r, s, a.V, tid & 31);
             if ((tid & 31) == 0) part[s] = sum;
         }
@@ -225,19 +208,74 @@ __global__ void __launch_bounds__(kPick) verify_pick_kernel(VerifyArgs a) {
         a.tokens[(size_t)b * (a.T + 1) + tid] = tid < k ? a.draft[(size_t)b * a.T + tid] : tid == k ? next : -1;
 }
 
+// The slices' sums of one sequence by `warps` warps, of which this is number w.
+template <bool VEC> __device__ __forceinline__ void sums(const VerifyArgs &a, const Rows &r, int w, int warps, double *part) {
+    const int ns = slices_of(a.V), lane = threadIdx.x & 31;
+    for (int s = w; s < ns; s += warps) {
+        const double sum = slice_sum<VEC>(r, s, a.V, lane);
+        if (lane == 0) part[s] = sum;
+    }
+}
+
+// A sequence by a cluster.
+template <bool VEC> __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
+    const int b = blockIdx.y, rank = blockIdx.x;
+    double *part = a.part + (size_t)b * slices_of(a.V);
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait_primary();
+    int n;
+    const int k = kept_drafts(a, b, threadIdx.x & 31, &n);
+    sums<VEC>(a, weight_rows(a, b, k, n), rank * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps, part);
+    // the sequence's sums are written, and seen by its first CTA
+    if (gridDim.x > 1) cluster_barrier();
+    else __syncthreads();
+    if (rank > 0) return;
+    if (threadIdx.x == 0) a.num_accepted[b] = k;
+    draw(a, b, k, n, part);
+}
+
+// The same in two kernels, sums and draw.
+template <bool VEC> __global__ void __launch_bounds__(kThreads) verify_sums_kernel(VerifyArgs a) {
+    const int b = blockIdx.y;
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait_primary();
+    int n;
+    const int k = kept_drafts(a, b, threadIdx.x & 31, &n);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.num_accepted[b] = k;
+    sums<VEC>(a, weight_rows(a, b, k, n), blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps,
+              a.part + (size_t)b * slices_of(a.V));
+}
+__global__ void __launch_bounds__(kThreads) verify_draw_kernel(VerifyArgs a) {
+    const int b = blockIdx.x;
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait_primary();
+    const int n = a.num_drafts ? min(max(a.num_drafts[b], 0), a.T) : a.T;
+    draw(a, b, a.num_accepted[b], n, a.part + (size_t)b * slices_of(a.V));
+}
+
 }  // namespace
 
 size_t verify_scratch_bytes(int B, int V) { return (size_t)B * slices_of(V) * sizeof(double); }
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
+    const int ns = slices_of(a.V);
+    const bool vec = a.V % 4 == 0 && (uintptr_t)a.target_probs % 16 == 0 && (uintptr_t)a.draft_probs % 16 == 0;
+    // One launch while the warps of a cluster have two slices each at most.  Called one by one (host included) and on
+    // the device, us: 1 sequence of V = 32,000 12.7 and 5.2, against 14.7 and 6.0 by two kernels; 8 of 100,003 12.7 and
+    // 8.2 against 14.7 and 7.5; 250 of 4096 12.7 and 5.9 against 14.7 and 8.6.  Beyond, more SMs count: 1 of 259,840
+    // would take 9.3 on the device against 6.2 by two kernels, 64 of them 27.8 against 25.5.
+    if (ns <= 2 * kMostCtas * kWarps) {
+        // CTAs of a sequence: until every warp has one slice at most, or every SM two CTAs
+        int ctas = 1;
+        while (ctas < kMostCtas && ctas * kWarps < ns && (long)a.B * ctas < 2 * 148) ctas *= 2;
+        return launch_clusters_after(vec ? verify_kernel<true> : verify_kernel<false>, ctas, dim3(ctas, a.B), kThreads, 0, s, a);
+    }
     // at most one wave of CTAs (8 per SM), every warp with as many slices as the others
-    const int need = (slices_of(a.V) + kWarps - 1) / kWarps, wave = (148 * 8 + a.B - 1) / a.B;
+    const int need = (ns + kWarps - 1) / kWarps, wave = (148 * 8 + a.B - 1) / a.B;
     const int rounds = (need + wave - 1) / wave;
     const dim3 grid((need + rounds - 1) / rounds, a.B);
-    const bool vec = a.V % 4 == 0 && (uintptr_t)a.target_probs % 16 == 0 && (uintptr_t)a.draft_probs % 16 == 0;
-    const cudaError_t e = launch_after(vec ? verify_sums_kernel<true> : verify_sums_kernel<false>, grid, 32 * kWarps, 0, s, a);
-    if (e != cudaSuccess) return e;
-    return launch_after(verify_pick_kernel, a.B, kPick, 0, s, a);
+    const cudaError_t e = launch_after(vec ? verify_sums_kernel<true> : verify_sums_kernel<false>, grid, kThreads, 0, s, a);
+    return e == cudaSuccess ? launch_after(verify_draw_kernel, a.B, kThreads, 0, s, a) : e;
 }
 
 }  // namespace rda

@@ -37,6 +37,17 @@ def test_equal_to_the_oracle(cuda_device, V, B, T):
     assert run(x, p, u) == latent.verify(x, p, u)
 
 
+@pytest.mark.parametrize("V", [8192, 8193, 9001, 16385, 40000, 65537, 131072, 131073, 131076])
+def test_vocabularies_around_the_changes_of_launch(cuda_device, V):
+    """One CTA, clusters of 2, 4 and 8, two kernels; and a residual of nothing in each."""
+    x, p, u, q = inputs(3, 2, V, seed=V)
+    assert run(x, p, u, q) == latent.verify(x, p, u, q)
+    same = p[:, :2].contiguous()                       # the target nowhere above the draft
+    never = torch.cat([torch.ones(3, 2), u[:, 2:]], 1) * 0.999999
+    x[:, 0] = -1                                       # refused, then drawn from the target itself
+    assert run(x, p, never, same) == latent.verify(x, p, never, same)
+
+
 def test_ragged_counts_and_bad_tokens(cuda_device):
     x, p, u, q = inputs(8, 5, 777, seed=2, near=0.05)
     n = torch.tensor([0, 1, 2, 3, 4, 5, 9, -3], dtype=torch.int32)
