@@ -424,9 +424,9 @@ def rda_verify_drafts_workspace_bytes(B, T, V) -> int:
 
 
 def _need_like(t, name, shape, dtype, dev):
-    """A contiguous tensor of this shape and type on CUDA device number ``dev``."""
+    """A contiguous tensor of this shape and type on CUDA device number ``dev``; returns its address."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("rda: tensors must be CUDA tensors (no CPU path exists)")
     if t.get_device() != dev:
@@ -446,10 +446,6 @@ def _device_of(t):
     return dev
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _scratch(workspace, dev):
     """(address, bytes) of a workspace tensor."""
     if workspace.get_device() != dev:
@@ -459,9 +455,10 @@ def _scratch(workspace, dev):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-# the current stream's handle without making a Stream object of it
+# the current stream's handle without making a Stream object of it, and the current device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launch(fn, dev, stream, *args):
@@ -473,7 +470,7 @@ def _launch(fn, dev, stream, *args):
         raise ValueError(f"rda: the stream belongs to device {stream.device_index}, the tensors to {dev}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         code = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -492,7 +489,8 @@ def _allocating_on(stream):
 
 
 def _latent_sizes(q, k, v, q_shared, k_shared, cu_q, cu_k):
-    """Checks the inputs of the expanded form; returns (total_q, total_k, H, Dk, Ds, Dv, N)."""
+    """Checks the inputs of the expanded form; returns (total_q, total_k, H, Dk, Ds, Dv, N), the
+    device's number, the type's code and the addresses of q, q_shared, k, k_shared, v, cu_q, cu_k."""
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or cu_q.dim() != 1 or cu_q.numel() < 1:
         raise ValueError("rda: q, k and v are [total, H, D], cu_seqlens [N + 1]")
     if (q_shared is None) != (k_shared is None):
@@ -501,19 +499,20 @@ def _latent_sizes(q, k, v, q_shared, k_shared, cu_q, cu_k):
     total_k, Dv = k.shape[0], v.shape[2]
     Ds = 0 if k_shared is None else k_shared.shape[-1]
     dev, dt = _device_of(q), q.dtype
-    _dtype_code(q)
-    _need_like(q, "q", (total_q, H, Dk), dt, dev)
-    _need_like(k, "k", (total_k, H, Dk), dt, dev)
-    _need_like(v, "v", (total_k, H, Dv), dt, dev)
+    code = _dtype_code(q)
+    p_q = _need_like(q, "q", q.shape, dt, dev)
+    p_k = _need_like(k, "k", (total_k, H, Dk), dt, dev)
+    p_v = _need_like(v, "v", (total_k, H, Dv), dt, dev)
+    p_qs = p_ks = None
     if Ds:
-        _need_like(q_shared, "q_shared", (total_q, H, Ds), dt, dev)
-        _need_like(k_shared, "k_shared", (total_k, Ds), dt, dev)
+        p_qs = _need_like(q_shared, "q_shared", (total_q, H, Ds), dt, dev)
+        p_ks = _need_like(k_shared, "k_shared", (total_k, Ds), dt, dev)
     elif k_shared is not None:
         raise ValueError("rda: pass no shared parts rather than empty ones")
     N = cu_q.numel() - 1
-    _need_like(cu_q, "cu_seqlens_q", (N + 1,), torch.int32, dev)
-    _need_like(cu_k, "cu_seqlens_k", (N + 1,), torch.int32, dev)
-    return total_q, total_k, H, Dk, Ds, Dv, N
+    p_cq = _need_like(cu_q, "cu_seqlens_q", (N + 1,), torch.int32, dev)
+    p_ck = p_cq if cu_k is cu_q else _need_like(cu_k, "cu_seqlens_k", (N + 1,), torch.int32, dev)
+    return (total_q, total_k, H, Dk, Ds, Dv, N), dev, code, (p_q, p_qs, p_k, p_ks, p_v, p_cq, p_ck)
 
 
 def rda_latent_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, scale, q_shared=None, k_shared=None,
@@ -530,22 +529,22 @@ def rda_latent_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, scale, q_sha
     """
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
-    total_q, total_k, H, Dk, Ds, Dv, N = sizes = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
-    dev = _device_of(q)
+    sizes, dev, code, inputs = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
+    total_q, total_k, H, Dk, Ds, Dv, N = sizes
     if out is not None:
         _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
     if lse is not None:
         _need_like(lse, "lse", (total_q, H), torch.float32, dev)
     with _allocating_on(stream):
         if out is None:
-            out = q.new_empty((total_q, H, Dv))
+            out = torch.empty_like(q) if Dv == Dk else q.new_empty((total_q, H, Dv))
         if lse is None and return_lse:
             lse = q.new_empty((total_q, H), dtype=torch.float32)
         if workspace is None:
             workspace = new_workspace(rda_latent_prefill_workspace_bytes(*sizes), q.device)
-    _launch(lib.rda_latent_prefill, dev, stream, _addr(q), _addr(q_shared), _addr(k), _addr(k_shared), _addr(v),
-            _addr(cu_seqlens_q), _addr(cu_seqlens_k), N, total_q, total_k, _addr(out), _addr(lse), _dtype_code(q),
-            H, Dk, Ds, Dv, float(scale), int(bool(causal)), *_scratch(workspace, dev))
+    _launch(lib.rda_latent_prefill, dev, stream, *inputs, N, total_q, total_k, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), code, H, Dk, Ds, Dv, float(scale), 1 if causal else 0,
+            *_scratch(workspace, dev))
     return out, lse
 
 
@@ -557,21 +556,20 @@ def rda_latent_backward(q, k, v, out, lse, d_out, cu_seqlens_q, cu_seqlens_k=Non
     Rows behind the last sequence are not written.  Deterministic."""
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
-    total_q, total_k, H, Dk, Ds, Dv, N = sizes = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
-    dev = _device_of(q)
-    _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
-    _need_like(d_out, "d_out", (total_q, H, Dv), q.dtype, dev)
-    _need_like(lse, "lse", (total_q, H), torch.float32, dev)
+    sizes, dev, code, inputs = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)
+    total_q, total_k, H, Dk, Ds, Dv, N = sizes
+    p_out = _need_like(out, "out", (total_q, H, Dv), q.dtype, dev)
+    p_dout = _need_like(d_out, "d_out", (total_q, H, Dv), q.dtype, dev)
+    p_lse = _need_like(lse, "lse", (total_q, H), torch.float32, dev)
     with _allocating_on(stream):
         g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                  dq_shared=torch.empty_like(q_shared) if Ds else None,
                  dk_shared=torch.empty_like(k_shared) if Ds else None)
         if workspace is None:
             workspace = new_workspace(rda_latent_backward_workspace_bytes(*sizes), q.device)
-    _launch(lib.rda_latent_backward, dev, stream, _addr(q), _addr(q_shared), _addr(k), _addr(k_shared), _addr(v),
-            _addr(out), _addr(lse), _addr(d_out), _addr(cu_seqlens_q), _addr(cu_seqlens_k), N, total_q, total_k,
-            _addr(g["dq"]), _addr(g["dq_shared"]), _addr(g["dk"]), _addr(g["dk_shared"]), _addr(g["dv"]),
-            _dtype_code(q), H, Dk, Ds, Dv, float(scale), int(bool(causal)), *_scratch(workspace, dev))
+    _launch(lib.rda_latent_backward, dev, stream, *inputs[:5], p_out, p_lse, p_dout, *inputs[5:], N, total_q, total_k,
+            *(None if g[n] is None else g[n].data_ptr() for n in ("dq", "dq_shared", "dk", "dk_shared", "dv")),
+            code, H, Dk, Ds, Dv, float(scale), 1 if causal else 0, *_scratch(workspace, dev))
     return g
 
 
@@ -591,12 +589,12 @@ def rda_latent_decode(q, pages, block_table, seq_lens, *, scale, q_shared=None, 
     Ds = 0 if q_shared is None else q_shared.shape[-1]
     dev, dt = _device_of(q), q.dtype
     code = _dtype_code(q)
-    _need_like(q, "q", (B, T, H, Dl), dt, dev)
-    if q_shared is not None:
-        _need_like(q_shared, "q_shared", (B, T, H, Ds), dt, dev)
-    _need_like(pages, "pages", (num_pages, page_size, Dl + Ds), dt, dev)
-    _need_like(block_table, "block_table", (B, block_table.shape[1]), torch.int32, dev)
-    _need_like(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    p_q = _need_like(q, "q", q.shape, dt, dev)
+    p_qs = None if q_shared is None else _need_like(q_shared, "q_shared", (B, T, H, Ds), dt, dev)
+    p_pages = _need_like(pages, "pages", (num_pages, page_size, Dl + Ds), dt, dev)
+    width = block_table.shape[1]
+    p_table = _need_like(block_table, "block_table", (B, width), torch.int32, dev)
+    p_lens = _need_like(seq_lens, "seq_lens", (B,), torch.int32, dev)
     if out is not None:
         _need_like(out, "out", (B, T, H, Dl), dt, dev)
     if lse is not None:
@@ -608,9 +606,9 @@ def rda_latent_decode(q, pages, block_table, seq_lens, *, scale, q_shared=None, 
             lse = q.new_empty((B, T, H), dtype=torch.float32)
         if workspace is None:
             workspace = new_workspace(rda_latent_decode_workspace_bytes(B, T, H, Dl, Ds), q.device)
-    _launch(lib.rda_latent_decode, dev, stream, _addr(q), _addr(q_shared), _addr(pages), _addr(block_table),
-            _addr(seq_lens), _addr(out), _addr(lse), code, B, T, H, Dl, Ds, num_pages, page_size,
-            block_table.shape[1], float(scale), *_scratch(workspace, dev))
+    _launch(lib.rda_latent_decode, dev, stream, p_q, p_qs, p_pages, p_table, p_lens, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), code, B, T, H, Dl, Ds, num_pages, page_size, width, float(scale),
+            *_scratch(workspace, dev))
     return out, lse
 
 
@@ -627,13 +625,11 @@ def rda_verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, nu
     B, T = draft_tokens.shape
     V = target_probs.shape[2]
     dev = _device_of(target_probs)
-    _need_like(draft_tokens, "draft_tokens", (B, T), torch.int32, dev)
-    _need_like(target_probs, "target_probs", (B, T + 1, V), torch.float32, dev)
-    _need_like(uniforms, "uniforms", (B, T + 1), torch.float32, dev)
-    if draft_probs is not None:
-        _need_like(draft_probs, "draft_probs", (B, T, V), torch.float32, dev)
-    if num_drafts is not None:
-        _need_like(num_drafts, "num_drafts", (B,), torch.int32, dev)
+    p_draft = _need_like(draft_tokens, "draft_tokens", draft_tokens.shape, torch.int32, dev)
+    p_target = _need_like(target_probs, "target_probs", (B, T + 1, V), torch.float32, dev)
+    p_u = _need_like(uniforms, "uniforms", (B, T + 1), torch.float32, dev)
+    p_q = None if draft_probs is None else _need_like(draft_probs, "draft_probs", (B, T, V), torch.float32, dev)
+    p_n = None if num_drafts is None else _need_like(num_drafts, "num_drafts", (B,), torch.int32, dev)
     if tokens is not None:
         _need_like(tokens, "tokens", (B, T + 1), torch.int32, dev)
     if num_accepted is not None:
@@ -645,8 +641,8 @@ def rda_verify_drafts(draft_tokens, target_probs, uniforms, draft_probs=None, nu
             num_accepted = draft_tokens.new_empty((B,))
         if workspace is None:
             workspace = new_workspace(rda_verify_drafts_workspace_bytes(B, T, V), target_probs.device)
-    _launch(lib.rda_verify_drafts, dev, stream, _addr(draft_tokens), _addr(draft_probs), _addr(target_probs),
-            _addr(uniforms), _addr(num_drafts), _addr(tokens), _addr(num_accepted), B, T, V, *_scratch(workspace, dev))
+    _launch(lib.rda_verify_drafts, dev, stream, p_draft, p_q, p_target, p_u, p_n, tokens.data_ptr(), num_accepted.data_ptr(),
+            B, T, V, *_scratch(workspace, dev))
     return tokens, num_accepted
 
 
