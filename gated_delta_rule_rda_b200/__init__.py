@@ -524,8 +524,8 @@ def rda_latent_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, scale, q_sha
     q_shared ``[total_q,H,Ds]`` and k_shared ``[total_k,Ds]`` (one key part for all heads), or
     neither; cu_seqlens int32 CUDA ``[N+1]`` (``cu_seqlens_k`` None: the queries').  ``causal``
     aligns a sequence's last query with its last key.  Returns ``(out [total_q,H,Dv], lse fp32
-    [total_q,H] or None)``; a query that sees no key gives zeros and -inf.  Rows behind the last
-    sequence are not written.
+    [total_q,H] or None)``; a query that sees no key gives zeros and -inf.  Rows outside the
+    sequences are not written.
     """
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
@@ -553,7 +553,7 @@ def rda_latent_backward(q, k, v, out, lse, d_out, cu_seqlens_q, cu_seqlens_k=Non
     """Gradients of ``<d_out, out>`` for :func:`rda_latent_prefill`, from its inputs, its
     ``out`` and its ``lse``.  Returns a dict of tensors like the inputs (their dtype): dq, dk, dv,
     dq_shared and dk_shared (None without shared parts; dk_shared is summed over the heads).
-    Rows behind the last sequence are not written.  Deterministic."""
+    Rows outside the sequences are not written.  Deterministic."""
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
     sizes, dev, code, inputs = _latent_sizes(q, k, v, q_shared, k_shared, cu_seqlens_q, cu_seqlens_k)

@@ -97,6 +97,7 @@ __device__ __forceinline__ int find_tile(const int32_t *cu, int num_seqs, int to
         else hi = mid - 1;
     }
     *t = slot - (clamped(cu, lo, total) / tile + lo);
+    if (*t < 0) *t = 0x3fffffff / tile;           // before the first sequence: behind every end
     return lo;
 }
 __host__ __device__ inline int tile_slots(int total, int num_seqs, int tile) { return total / tile + num_seqs; }

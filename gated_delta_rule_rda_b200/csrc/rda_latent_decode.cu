@@ -743,6 +743,7 @@ template <bool MANY> __global__ void __launch_bounds__(kJoin) latent_join_bf16_k
     pdl_wait_primary();
     const int4 rec = parts.rec[blockIdx.x];
     if (rec.x < 0 || !on) return;
+    if (rec.x >= a.B || rec.w < 0 || rec.y < rec.w || rec.y >= g.groups) return;      // never written
     const int n = rec.y - rec.w + 1;
     auto slot = [&](int i) { return (((size_t)(rec.w + i) * g.rt + rt) * 2 + (i == 0 ? rec.z : 0)) * g.nt + r; };
     auto part = [&](int i) {

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(256) latent_shared_sum_kernel(const float *par
     ptx::pdl_wait_primary();
     const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
     const long row = e / Ds;
-    if (row >= rows || row >= cu_k[num_seqs]) return;
+    if (row >= rows || row < cu_k[0] || row >= cu_k[num_seqs]) return;
     const int c = (int)(e % Ds);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -447,7 +447,7 @@ int forward_splits(int total_q, int total_k, int H) {
     return (int)std::max(1L, std::min({want, tiles, 8L}));
 }
 
-__global__ void latent_join_kernel(LatentDecodeArgs a, int splits, const int32_t *end);
+__global__ void latent_join_kernel(LatentDecodeArgs a, int splits, const int32_t *cu, int num_seqs);
 
 template <typename T, int NDV, int RI, int NT> cudaError_t forward_ri(const LatentArgs &a, int splits, cudaStream_t s) {
     constexpr int M = RI * NT / 16;
@@ -463,7 +463,7 @@ template <typename T, int NDV, int RI, int NT> cudaError_t forward_ri(const Late
     LatentDecodeArgs j{};
     j.B = a.total_q, j.T = 1, j.H = a.H, j.Dl = 64 * NDV;
     j.out = a.out, j.lse = a.lse, j.part = a.delta;
-    latent_join_kernel<<<a.total_q * a.H, 128, 0, s>>>(j, splits, a.cu_q + a.num_seqs);
+    latent_join_kernel<<<a.total_q * a.H, 128, 0, s>>>(j, splits, a.cu_q, a.num_seqs);
     return cudaGetLastError();
 }
 template <typename T, int NDV> cudaError_t forward_nv(const LatentArgs &a, cudaStream_t s) {
@@ -674,10 +674,10 @@ __global__ void __launch_bounds__(16 * ROWS) latent_decode_f32_kernel(LatentDeco
 }
 
 // out = sum_s e^{lse_s - lse} o_s, lse = log sum_s e^{lse_s}: one CTA per row.
-// Rows of tokens from *end on (where given) are left as they were.
-__global__ void __launch_bounds__(128) latent_join_kernel(LatentDecodeArgs a, int splits, const int32_t *end) {
+// Rows of tokens outside the sequences of `cu` (where given) are left as they were.
+__global__ void __launch_bounds__(128) latent_join_kernel(LatentDecodeArgs a, int splits, const int32_t *cu, int num_seqs) {
     const size_t row = blockIdx.x;
-    if (end && (long)(row / a.H) >= (long)*end) return;
+    if (cu && ((long)(row / a.H) < (long)cu[0] || (long)(row / a.H) >= (long)cu[num_seqs])) return;
     const float *ls = a.part + row * splits;
     const float *po = a.part + (((size_t)a.B * a.T * a.H * splits + 3) & ~(size_t)3) + row * splits * a.Dl;
     float top = -INFINITY, sum = 0.f;
@@ -715,7 +715,7 @@ template <int NL, int ROWS> cudaError_t decode_rows_nl(const LatentDecodeArgs &a
     const size_t bytes = sizeof(float) * ((ROWS + 2 * kDecTok) * (128 * NL + a.Ds + 4) + extra);
     latent_decode_f32_kernel<NL, ROWS><<<dim3(splits * a.B, (R + ROWS - 1) / ROWS), 16 * ROWS, bytes, s>>>(a, splits);
     if ((e = cudaGetLastError()) != cudaSuccess || splits == 1) return e;
-    latent_join_kernel<<<a.B * R, 128, 0, s>>>(a, splits, nullptr);
+    latent_join_kernel<<<a.B * R, 128, 0, s>>>(a, splits, nullptr, 0);
     return cudaGetLastError();
 }
 template <int NL> cudaError_t decode_nl(const LatentDecodeArgs &a, cudaStream_t s) {

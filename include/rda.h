@@ -423,9 +423,10 @@ rda_status_t rda_prefill_chunked_noalloc(const void *q, const void *k, const voi
  *
  *   q [total_q,H,Dk], k [total_k,H,Dk], v [total_k,H,Dv], out [total_q,H,Dv]: device, dtype
  *   q_shared [total_q,H,Ds], k_shared [total_k,Ds]: device, dtype; NULL exactly when Ds = 0
- *   cu_seqlens_q, cu_seqlens_k  device int32 [num_seqs+1], non-decreasing from 0 to at most
- *                  total_q, total_k (values are kept inside these bounds).  Rows
- *                  behind the last sequence are neither read into a result nor written
+ *   cu_seqlens_q, cu_seqlens_k  device int32 [num_seqs+1], non-decreasing, in [0, total_q]
+ *                  and [0, total_k] (values are kept inside these bounds).  Rows before
+ *                  the first sequence and behind the last are neither read into a result
+ *                  nor written
  *   lse            device fp32 [total_q,H] or NULL
  *   Dk, Dv in {64, 128}, Ds in {0, 64}, H <= 1024; total * H * (Dk + Ds) and
  *                  (total + num_seqs) * H below 2^31

@@ -139,6 +139,36 @@ def test_gradients_write_no_row_behind_the_last_sequence(cuda_device):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lead", [3, 400])
+def test_sequences_in_the_middle_of_a_batch(cuda_device, dtype, lead):
+    """Offsets that begin behind 0: only the sequences they name are computed and written."""
+    lens = [lead, 130, 300, 77]
+    x = packed(lens, lens, 2, 128, 64, 128, dtype, seed=14)
+    d, (lo, hi) = dev(x), (lead, lead + 430)
+    part = {**d, "cu_q": d["cu_q"][1:4].contiguous(), "cu_k": d["cu_k"][1:4].contiguous()}
+    whole, wl = forward(d)
+    out = torch.full_like(whole, 7.0)
+    lse = torch.full_like(wl, 7.0)
+    forward(part, out=out, lse=lse)
+    r, rg = oracle_forward(x, True), oracle_gradients(x, True)
+    check(out[lo:hi], r["out"][lo:hi], r["out_round"][lo:hi], dtype, 192, x["scale"], 300, "out")
+    for t in (out, lse):
+        assert (t[:lo] == 7).all() and (t[hi:] == 7).all()
+    lib, P = rda.lib, rda._ptr
+    g = {n: torch.full_like(d[n], 7.0) for n in ("q", "q_shared", "k", "k_shared", "v")}
+    total = sum(lens)
+    ws = rda.new_workspace(rda.rda_latent_backward_workspace_bytes(total, total, 2, 128, 64, 128, 2), "cuda")
+    assert lib.rda_latent_backward(P(d["q"]), P(d["q_shared"]), P(d["k"]), P(d["k_shared"]), P(d["v"]), P(whole), P(wl),
+                                   P(d["d_out"]), P(part["cu_q"]), P(part["cu_k"]), 2, total, total, P(g["q"]),
+                                   P(g["q_shared"]), P(g["k"]), P(g["k_shared"]), P(g["v"]), rda._dtype_code(d["q"]), 2, 128,
+                                   64, 128, x["scale"], 1, P(ws), ws.numel(), rda._stream(None)) == 0
+    torch.cuda.synchronize()
+    for n, t in g.items():
+        assert (t[:lo] == 7).all() and (t[hi:] == 7).all(), n
+        check(t[lo:hi], rg["d" + n][lo:hi], rg["d" + n + "_round"][lo:hi], dtype, 192, x["scale"], 900, n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_offsets_out_of_bounds_stay_inside(cuda_device, dtype):
     """cu_seqlens that a caller got wrong are kept inside the tensors."""
     x = packed([50], [50], 1, 64, 0, 64, dtype, seed=13)
