@@ -322,6 +322,33 @@ def test_decode_many_short_sequences(cuda_device, dtype):
     check_absorbed(x, out, lse, dtype)
 
 
+def test_decode_most_rows(cuda_device):
+    """8 tokens of 1024 heads: more row tiles than the batch can be split for."""
+    x = paged([70, 9], 8, 1024, 128, 64, 16, BF16, seed=94)
+    out, lse = absorbed(dev(x))
+    check_absorbed(x, out, lse, BF16)
+
+
+def test_decode_largest_batch(cuda_device):
+    B, Dl, page = 65535, 128, 16
+    g = torch.Generator(device="cuda").manual_seed(95)
+    pages = torch.randn(3000, page, Dl, generator=g, device="cuda").to(BF16)
+    table = torch.randint(0, 3000, (B, 2), generator=g, device="cuda", dtype=torch.int32)
+    lens = torch.randint(0, 33, (B,), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn(B, 1, 1, Dl, generator=g, device="cuda").to(BF16)
+    scale = Dl ** -0.5
+    out, lse = rda.rda_latent_decode(q, pages, table, lens, scale=scale, return_lse=True)
+    for lo in range(0, B, 8192):                       # the definition in 64 bits, a part at a time
+        c = pages[table[lo:lo + 8192].long()].flatten(1, 2).double()
+        s = scale * (c @ q[lo:lo + 8192, 0, 0].double()[..., None])[..., 0]
+        s = s.masked_fill(torch.arange(32, device="cuda") >= lens[lo:lo + 8192, None], -math.inf)
+        p = torch.nan_to_num(torch.softmax(s, 1))      # no token: no weight
+        ref = (p[:, None] @ c)[:, 0]
+        moved = (p[:, None] @ c.abs())[:, 0] + ref.abs()
+        check(out[lo:lo + 8192, 0, 0], ref.cpu(), moved.cpu(), BF16, Dl, scale, 32, "out")
+        check_lse(lse[lo:lo + 8192, 0, 0], torch.logsumexp(s, 1).cpu(), Dl, scale)
+
+
 def test_decode_cache_past_32_bit_offsets(cuda_device):
     """A cache of more than 2^32 bytes and 2^31 elements, with the sequence's pages at its end."""
     D, page = 576, 64
