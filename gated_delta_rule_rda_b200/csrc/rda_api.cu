@@ -89,9 +89,9 @@ const char *rda_status_string(rda_status_t s) {
     switch (s) {
         case RDA_OK: return "RDA_OK";
         case RDA_ERR_INVALID_ARG: return "RDA_ERR_INVALID_ARG: null required pointer, negative size or bad cu_seqlens";
-        case RDA_ERR_UNSUPPORTED: return "RDA_ERR_UNSUPPORTED: Dk and Dv must be 64 or 128; dtype must be RDA_F32 or RDA_BF16";
+        case RDA_ERR_UNSUPPORTED: return "RDA_ERR_UNSUPPORTED: a size outside those the call supports (Dk and Dv must be 64 or 128), or dtype not RDA_F32 or RDA_BF16";
         case RDA_ERR_MISALIGNED: return "RDA_ERR_MISALIGNED: q, k, v, out, state and workspace must be 16-byte aligned (workspace 256)";
-        case RDA_ERR_WORKSPACE: return "RDA_ERR_WORKSPACE: workspace missing or smaller than rda_prefill_workspace_bytes()";
+        case RDA_ERR_WORKSPACE: return "RDA_ERR_WORKSPACE: workspace missing or smaller than the call's rda_..._workspace_bytes()";
         case RDA_ERR_CUDA: return "RDA_ERR_CUDA: a CUDA runtime call or kernel launch failed";
         case RDA_ERR_TIMEOUT: return "RDA_ERR_TIMEOUT: a bounded device-side wait ran out";
     }

@@ -78,7 +78,7 @@ extern "C" {
 typedef enum {
     RDA_OK = 0,
     RDA_ERR_INVALID_ARG = 1,   /* null required pointer, negative size, bad cu_seqlens */
-    RDA_ERR_UNSUPPORTED = 2,   /* Dk or Dv outside {64, 128}, unknown dtype          */
+    RDA_ERR_UNSUPPORTED = 2,   /* a size the call does not support, unknown dtype    */
     RDA_ERR_MISALIGNED = 3,    /* a pointer breaks the 16-byte alignment rule        */
     RDA_ERR_WORKSPACE = 4,     /* workspace missing or smaller than required         */
     RDA_ERR_CUDA = 5,          /* a CUDA runtime call or kernel launch failed        */
