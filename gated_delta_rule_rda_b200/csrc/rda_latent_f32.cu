@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(NT) latent_forward_f32_kernel(LatentArgs a, in
 //
 // 4 x 8 lanes a warp: with RI = 4 a thread's products over four columns read six
 // 128-byte rows of shared memory for 32 FMAs a lane, its sums 16 for 192.  RI = 2
-// makes twice the CTAs, where 64 rows each would leave SMs empty.
+// makes twice the CTAs, where 64 rows each would leave SMs empty (80 tiles of 64: 177
+// us against 231; 120: 470 and 614; but 240 of them: 821 and 620).
 // Measured (16 heads of 128 + 64 and 128, T = 900, causal): 621 us for both sides, 899
 // with a head's tiles side by side instead of the heads (an SM idle for half the
 // time), 997 without the copies meanwhile and with 2 x 16 lanes a warp.
