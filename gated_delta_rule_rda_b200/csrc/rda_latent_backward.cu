@@ -613,6 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     delta += B.lack[0][r] + B.lack[1][r];
                     if (half == 0 && r < rows) st[kStat] = delta;
                 }
+                // not two phases ahead of the thread that waits for them: it tells them apart by parity alone
+                if (i > 0) w.wait(&B.dq_done, (i - 1) & 1);
                 mbar_arrive(&B.ds_ready);
                 p.next(kStK);
                 continue;
