@@ -193,7 +193,8 @@ __device__ __forceinline__ void draw(const VerifyArgs &a, int b, int k, int n, d
     }
     const double four = w[0] + w[1] + w[2] + w[3];
     double sum;
-    double at = block_scan(four, warp_s, &sum) - four + start_s;      // its barriers publish start_s
+    const double upto4 = block_scan(four, warp_s, &sum);
+    double at = upto4 - four + start_s;      // read behind the scan, whose barriers publish it
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
         at += w[v];
