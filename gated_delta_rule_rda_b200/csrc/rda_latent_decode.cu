@@ -212,7 +212,7 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
     const Waiter w = x_.w;
     Walk walk = x_.walk;
     uint8_t *p_s = x_.p_s;
-    const int NP = a.Dl / 128, R = a.T * a.H;
+    const int NP = a.Dl / 128, NS = NP / g.sp, R = a.T * a.H;
     const int rt = x_.rt, grp = x_.grp, row0 = x_.row0, rows = x_.rows;
     const long long hi = x_.hi, total = x_.total;
     const int c0 = half ? split_cols(NT) : 0, bar = 1 + half;
@@ -224,6 +224,7 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
     const float sc = a.scale * kLog2e;
     constexpr int C = NC / 8;
     uint32_t it = 0;
+    RingPos ring;                                    // a tile's first slot
     const Parts parts = parts_of(a.part, g, a.Dl);
     bool first_segment = true;
     while (walk.next(a)) {
@@ -250,7 +251,9 @@ __device__ __forceinline__ void softmax(const SoftmaxCtx<NT> &x_, int half) {
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) v[c][u] *= sc;       // log2 units; sc may be negative
+            w.wait(&S.full[ring.slot], ring.phase);             // the masks, written beside the copies
             const uint2 seen = *reinterpret_cast<const uint2 *>(S.seen[it % kInfo]);
+            ring.skip(NS, g.slots);
             const int j0 = t * kTok + 16 * quad + tok;
             const bool whole = (seen.x & seen.y) == 0xffffffffu && t * kTok + kTok - 1 <= all_see;
             if (!whole) {
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
         tmem_relinquish();
     }
     if (tid == 32) {
-        for (int i = 0; i < g.slots; ++i) mbar_init(&S.full[i], 32 * kCopyWarps), mbar_init(&S.empty[i], 1);
+        for (int i = 0; i < g.slots; ++i) mbar_init(&S.full[i], 33 * kCopyWarps), mbar_init(&S.empty[i], 1);
         mbar_init(&S.q_full, 1);
         mbar_init(&S.q_empty, 1);
         mbar_init(&S.s_full[0], 1);
@@ -677,6 +680,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
                         if (++sr == g.shared) sr = 0;
                     }
                     cp_async_arrive(smem_u32(&S.full[pr.slot]));
+                    // that arrival stands for copies alone: what lane 0 has written to `seen` is published by one of its own
+                    if (lane == 0) mbar_arrive(&S.full[pr.slot]);
                     pr.next(g.slots);
                 }
                 // the next tile's tokens come as far as L2 while this warp waits for room

@@ -95,6 +95,10 @@ struct RingPos {
     __device__ __forceinline__ void next(int n) {
         if (++slot == n) slot = 0, phase ^= 1;
     }
+    // `by` slots on, n of them at most
+    __device__ __forceinline__ void skip(int by, int n) {
+        if ((slot += by) >= n) slot -= n, phase ^= 1;
+    }
 };
 
 // D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate (A: one row per lane, two values a column).

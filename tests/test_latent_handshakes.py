@@ -19,11 +19,12 @@ def wait(bar, phase):
 def explore(roles, counts):
     """Walks all interleavings of `roles` ({name: steps}); `counts`: arrivals that complete a phase (1 where not given).
     Steps: ("wait", bar, phase), ("arrive", bar), ("copy", bar, place, tag), ("mma", reads, writes) and ("commit", bar)
-    (both asynchronous, in a role's order), ("read", place, tag), ("write", place, tag)."""
+    (both asynchronous, in a role's order), ("read", place, tag), ("write", place, tag), and ("note", place, tag): a write
+    that others may rely on from the role's next own arrival on, as a copy's arrival or a commit's does not publish it."""
     progs = list(roles.values())
     bars = sorted({s[1] for p in progs for s in p if s[0] in ("wait", "arrive", "copy", "commit")})
     index = {b: i for i, b in enumerate(bars)}
-    places = sorted({s[2] for p in progs for s in p if s[0] == "copy"} | {s[1] for p in progs for s in p if s[0] in ("read", "write")} |
+    places = sorted({s[2] for p in progs for s in p if s[0] == "copy"} | {s[1] for p in progs for s in p if s[0] in ("read", "write", "note")} |
                     {x for p in progs for s in p if s[0] == "mma" for part in s[1:] for x, _ in part})
     where = {x: i for i, x in enumerate(places)}
     need = [counts.get(b, 1) for b in bars]
@@ -32,7 +33,15 @@ def explore(roles, counts):
     for p, prog in enumerate(progs):
         for i, s in enumerate(prog):
             before[p][i + 1] = before[p][i] + (s[0] in ("mma", "commit"))
-    # state: steps done by each role, MMAs and commits completed of each, copies in flight, (phases, arrivals), tags
+    notes = []                                       # what an arrival publishes, by role and step
+    for prog in progs:
+        notes.append([])
+        held = []
+        for s in prog:
+            notes[-1].append(tuple(held))
+            held = [] if s[0] == "arrive" else held + [s[1:]] if s[0] == "note" else held
+    # state: steps done by each role, MMAs and commits completed of each, copies in flight, (phases, arrivals), tags; what
+    # a role has noted and not published follows from its steps
     start = ((0,) * len(progs), (0,) * len(progs), frozenset(), ((0, 0),) * len(bars), (None,) * len(places))
 
     def arrive(state, b):
@@ -50,6 +59,11 @@ def explore(roles, counts):
 
     def moves(state):
         pcs, fin, copies, bs, tags = state
+        for p, prog in enumerate(progs):
+            # nobody sees a commit's issue or a note: taken at once
+            if pcs[p] < len(prog) and prog[pcs[p]][0] in ("commit", "note"):
+                yield (pcs[:p] + (pcs[p] + 1,) + pcs[p + 1:], fin, copies, bs, tags)
+                return
         for p, prog in enumerate(progs):
             if fin[p] < before[p][pcs[p]]:
                 s = issued[p][fin[p]]
@@ -77,7 +91,10 @@ def explore(roles, counts):
                 elif done > s[2]:
                     raise Fault(f"{s[1]} shut behind phase {s[2]}: {done} complete")
             elif s[0] == "arrive":
-                yield (nxt, fin, copies, arrive(bs, s[1]), tags)
+                t = tags
+                for x, tag in notes[p][pcs[p]]:
+                    t = put(t, x, tag)
+                yield (nxt, fin, copies, arrive(bs, s[1]), t)
             elif s[0] == "copy":
                 yield (nxt, fin, copies | {s[1:]}, bs, put(tags, s[2], "arriving"))
             elif s[0] == "read":
@@ -86,7 +103,7 @@ def explore(roles, counts):
                 yield (nxt, fin, copies, bs, tags)
             elif s[0] == "write":
                 yield (nxt, fin, copies, bs, put(tags, s[1], s[2]))
-            elif s[0] == "mma":
+            else:
                 t = tags
                 for x, tag in s[1]:
                     if tags[where[x]] != tag:
@@ -94,8 +111,6 @@ def explore(roles, counts):
                 for x, tag in s[2]:
                     t = put(t, x, ("under way", tag))
                 yield (nxt, fin, copies, bs, t)
-            else:
-                yield (nxt, fin, copies, bs, tags)
         for c in copies:
             yield (pcs, fin, copies - {c}, arrive(bs, c[0]), put(tags, c[1], c[2]))
 
@@ -231,6 +246,69 @@ def prefill_roles(n0, n1, stages=2):
     return dict(produce=produce, scores=scores, values=values, s0=soft[0], s1=soft[1]), {}
 
 
+def decode_roles(segments, shared, publishes=True, slots=4, ns=2):
+    """latent_decode_kernel: segments of as many tiles, a tile in `ns` slots, two copying warps and two halves of the
+    softmax.  The MMA thread takes what can go next: a role for the scores and one for the values, which knows more
+    orders than the thread has.  `publishes`: the copying warps arrive for their masks themselves."""
+    copy, scores, values, soft, queries = [[], []], [], [], [[], []], []
+    it = 0
+    for seg, tiles in enumerate(segments):
+        if seg:
+            queries.append(wait("q_empty", seg - 1))
+        queries.append(("copy", "q_full", "Q", seg))
+        for t in range(tiles):
+            first = it * ns % slots
+            for w, c in enumerate(copy):
+                c.append(("note", f"seen{it % 16}.{w}", it))
+                for n in range(ns):
+                    at = it * ns + n
+                    if n == ns - 1 and it >= shared:
+                        c.append(wait(f"s_full{(it - shared) & 1}", (it - shared) >> 1))
+                    if at >= slots:
+                        c.append(wait(f"empty{at % slots}", at // slots - 1))
+                    c.append(("copy", f"full{at % slots}", f"L{at % slots}.{w}", it))
+                    if n == ns - 1:
+                        c.append(("copy", f"full{at % slots}", f"R{it % shared}.{w}", it))
+                    if publishes:
+                        c.append(("arrive", f"full{at % slots}"))
+            if it >= 2:
+                scores.append(wait(f"values{it - 2}", 0))
+            for n in range(ns):
+                at = it * ns + n
+                scores.append(wait(f"full{at % slots}", at // slots))
+                if t == 0 and n == 0:
+                    scores.append(wait("q_full", seg))
+                own = [(f"L{at % slots}.{w}", it) for w in (0, 1)]
+                if n == ns - 1:
+                    own += [(f"R{it % shared}.{w}", it) for w in (0, 1)]
+                scores.append(("mma", (("Q", seg), *own), ((f"S{it & 1}.0", it), (f"S{it & 1}.1", it))))
+            scores += [("commit", f"s_full{it & 1}"), ("arrive", f"scores{it}")]
+            if t == tiles - 1:
+                scores.append(("commit", "q_empty"))
+            values += [wait(f"scores{it}", 0), wait("p_ready", it)]
+            if t == 0 and seg:
+                values.append(wait("o_empty", seg - 1))
+            for n in range(ns):
+                at = it * ns + n
+                own = [(f"L{at % slots}.{w}", it) for w in (0, 1)]
+                values += [("mma", (("P0", it), ("P1", it), *own), ((f"O{n}", it),)), ("commit", f"empty{at % slots}")]
+            values += [("commit", "pv_done"), ("arrive", f"values{it}")]
+            for h, e in enumerate(soft):
+                e += [wait(f"s_full{it & 1}", it >> 1), ("read", f"S{it & 1}.{h}", it), wait(f"full{first}", it * ns // slots),
+                      ("read", f"seen{it % 16}.0", it), ("read", f"seen{it % 16}.1", it)]
+                if it:
+                    e.append(wait("pv_done", it - 1))
+                    e += [("read", f"O{n}", it - 1) for n in range(ns) if t]
+                e += [("write", f"P{h}", it), ("arrive", "p_ready")]
+            it += 1
+        for e in soft:
+            e += [wait("pv_done", it - 1), *(("read", f"O{n}", it - 1) for n in range(ns)), ("arrive", "o_empty")]
+    counts = dict.fromkeys(("p_ready", "o_empty"), 2)
+    for i in range(slots):
+        counts[f"full{i}"] = 2 * ((2 if i % ns == ns - 1 else 1) + publishes)
+    return dict(c0=copy[0], c1=copy[1], scores=scores, values=values, s0=soft[0], s1=soft[1], queries=queries), counts
+
+
 @pytest.mark.parametrize("tiles", [1, 2, 3, 4])
 def test_dq(tiles):
     """1 and 2 key tiles have a pass ahead, more do not."""
@@ -252,3 +330,13 @@ def test_dkv(steps):
 @pytest.mark.parametrize("n0,n1", [(1, 1), (0, 2), (2, 0), (1, 3), (3, 3)])
 def test_prefill(n0, n1):
     assert explore(*prefill_roles(n0, n1)) > 20
+
+
+@pytest.mark.parametrize("segments,shared,ns", [((3,), 1, 1), ((1, 1), 2, 1), ((2,), 1, 2)])
+def test_decode(segments, shared, ns):
+    assert explore(*decode_roles(segments, shared, slots=2 * ns, ns=ns)) > 100
+
+
+def test_decode_whose_masks_nobody_publishes():
+    with pytest.raises(Fault, match="seen"):
+        explore(*decode_roles((1,), 1, publishes=False))
