@@ -26,3 +26,60 @@ def test_gradients_whose_delta_is_formed_again(cuda_device):
         g2 = gradients(d, out, lse, workspace=ws)
         assert all(torch.equal(g[n], g2[n]) for n in NAMES)
     assert rda.rda_read_device_error(ws) == 0
+
+
+def compare(x, causal, what=NAMES):
+    """Forward and gradients of packed inputs against the oracle; returns them."""
+    lq, lk = x["cu_q"].diff(), x["cu_k"].diff()
+    D, dtype = x["q"].shape[2] + (x["q_shared"].shape[2] if x["q_shared"] is not None else 0), x["q"].dtype
+    d = dev(x)
+    ws = rda.new_workspace(1 << 28, "cuda")
+    out, lse = forward(d, causal=causal, workspace=ws)
+    r, rg = oracle_forward(x, causal), oracle_gradients(x, causal)
+    check(out, r["out"], r["out_round"], dtype, D, x["scale"], int(lk.max()), "out")
+    check_lse(lse, r["lse"], D, x["scale"])
+    g = gradients(d, out, lse, causal=causal, workspace=ws)
+    for n in what:
+        if n in rg:
+            check(g[n], rg[n], rg[n + "_round"], dtype, D, x["scale"], 3 * int(max(lq.max(), lk.max())), n)
+    assert rda.rda_read_device_error(ws) == 0
+    out2, lse2 = forward(d, causal=causal, workspace=ws)
+    g2 = gradients(d, out, lse, causal=causal, workspace=ws)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and all(g[n] is None or torch.equal(g[n], g2[n]) for n in g)
+    return d, out, lse, g
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Dk,Ds,Dv", [(128, 64, 128), (64, 0, 64), (64, 64, 128), (128, 0, 64)])
+@pytest.mark.parametrize("lens", [
+    [100, 1, 90],          # 3 x 37 tiles of 64 rows: 16 rows a CTA forward, 32 in the gradients
+    [101, 1, 90],          # 4 x 37 = 148: 64 and 64
+    [330, 0, 301, 8],      # 5 x 37 tiles of 128: 64
+    [331, 0, 301, 8],      # 6 x 37 = 222: 128
+])
+def test_fp32_rows_of_a_cta(cuda_device, lens, Dk, Ds, Dv, causal):
+    """fp32 on either side of each change in the rows that a CTA takes."""
+    compare(packed(lens, lens, 37, Dk, Ds, Dv, F32, seed=sum(lens) + Dk + Ds + Dv), causal)
+
+
+@pytest.mark.parametrize("lq,lk", [([60, 3, 0, 70], [500, 131, 64, 70]), ([400, 130, 65, 70], [40, 130, 0, 1])])
+def test_fp32_queries_and_keys_that_differ(cuda_device, lq, lk):
+    """Few rows on one side and many on the other: each side's gradients by kernels of their own size."""
+    compare(packed(lq, lk, 40, 128, 64, 128, F32, seed=len(lk) + lk[0]), True)
+
+
+def test_fp32_rows_behind_the_last_sequence_many_heads(cuda_device):
+    """NaN behind the sequences of a batch that 64 and 128 rows a CTA take."""
+    for lens, pad in (([130, 77, 64], 30), ([300, 257, 1, 90], 100)):
+        x = packed(lens, lens, 40, 128, 64, 128, F32, seed=pad, pad=pad)
+        d, n = dev(x), sum(lens)
+        out = torch.full((n + pad, 40, 128), 7.0, device="cuda")
+        lse = torch.full((n + pad, 40), 7.0, device="cuda")
+        forward(d, out=out, lse=lse)
+        y = {m: t[:n] if isinstance(t, torch.Tensor) and len(t) == n + pad else t for m, t in x.items()}
+        r, rg = oracle_forward(y, True), oracle_gradients(y, True)
+        assert (out[n:] == 7).all() and (lse[n:] == 7).all()
+        check(out[:n], r["out"], r["out_round"], F32, 192, x["scale"], 300, "out")
+        g = gradients(d, out, lse)
+        for m in NAMES:
+            check(g[m][:n], rg[m], rg[m + "_round"], F32, 192, x["scale"], 900, m)
