@@ -83,3 +83,67 @@ def test_fp32_rows_behind_the_last_sequence_many_heads(cuda_device):
         g = gradients(d, out, lse)
         for m in NAMES:
             check(g[m][:n], rg[m], rg[m + "_round"], F32, 192, x["scale"], 900, m)
+
+
+def alone(x, n):
+    """Sequence n of packed inputs by itself (device tensors), and the rows of its queries and keys."""
+    sq, sk = slice(*x["cu_q"][n:n + 2].tolist()), slice(*x["cu_k"][n:n + 2].tolist())
+    one = {m: t[sk if m in ("k", "v", "k_shared") else sq].contiguous() if isinstance(t, torch.Tensor) else t
+           for m, t in x.items()}
+    one["cu_q"], one["cu_k"] = cu([sq.stop - sq.start], "cuda"), cu([sk.stop - sk.start], "cuda")
+    return one, sq, sk
+
+
+@pytest.mark.parametrize("lq,lk", [
+    ([300, 77, 5], [300, 77, 5]),                              # 4 places x 37 heads = 148 CTAs: by their places
+    ([300, 77, 0, 5], [300, 77, 0, 5]),                        # 5 x 37: in order
+    ([700, 0, 33, 513, 256, 1], [700, 40, 161, 600, 256, 0]),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_bf16_tiles_in_order(cuda_device, lq, lk, causal):
+    """Tiles ordered by their work and not: the oracle's results, and each sequence's bits are those of a call by itself."""
+    x = packed(lq, lk, 37, 128, 64, 128, BF16, seed=len(lq) + causal)
+    d, out, lse, g = compare(x, causal)
+    for n in range(len(lq)):
+        one, sq, sk = alone(d, n)
+        if not lq[n] or not lk[n]:
+            continue
+        o1, l1 = forward(one, causal=causal)
+        g1 = gradients(one, o1, l1, causal=causal)
+        assert torch.equal(o1, out[sq]) and torch.equal(l1, lse[sq])
+        assert all(torch.equal(g1[m], g[m][sq if m in ("dq", "dq_shared") else sk]) for m in NAMES)
+
+
+@pytest.mark.parametrize("count,H", [(600, 1), (1100, 1), (1100, 2)])
+def test_bf16_more_sequences_than_threads(cuda_device, count, H):
+    """More tiles than the ordering CTA has threads (512 and 256), and more sequences than it keeps offsets of (1024);
+    empty sequences among them, and some of several tiles."""
+    lq = [(7 * i) % 13 if i % 97 else 300 + i % 5 for i in range(count)]
+    lk = [n + i % 3 if i % 11 else 0 for i, n in enumerate(lq)]
+    x = packed(lq, lk, H, 64, 64, 64, BF16, seed=count + H)
+    d, out, lse, g = compare(x, True)
+    for n in (0, 1, 97, 98, count - 2):
+        one, sq, sk = alone(d, n)
+        if not lq[n] or not lk[n]:
+            continue
+        o1, l1 = forward(one)
+        g1 = gradients(one, o1, l1)
+        assert torch.equal(o1, out[sq]) and torch.equal(l1, lse[sq])
+        assert all(torch.equal(g1[m], g[m][sq if m in ("dq", "dq_shared") else sk]) for m in NAMES)
+
+
+def test_fp32_alone_and_packed(cuda_device):
+    """fp32 splits keys by the whole batch's size: a sequence's results are the same bits from run to run (`compare`), and
+    alone and packed both within the bound."""
+    lens = [257, 64, 190]
+    x = packed(lens, lens, 2, 128, 64, 128, F32, seed=14)
+    d, _, _, _ = compare(x, True)
+    r, rg = oracle_forward(x, True), oracle_gradients(x, True)
+    for n in range(3):
+        one, s, _ = alone(d, n)
+        o1, l1 = forward(one)
+        check(o1, r["out"][s], r["out_round"][s], F32, 192, x["scale"], 257, "out")
+        check_lse(l1, r["lse"][s], 192, x["scale"])
+        g1 = gradients(one, o1, l1)
+        for m in NAMES:
+            check(g1[m], rg[m][s], rg[m + "_round"][s], F32, 192, x["scale"], 900, m)
