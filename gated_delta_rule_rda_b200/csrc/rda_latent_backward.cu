@@ -688,7 +688,7 @@ cudaError_t launch_latent_backward_tc(const LatentArgs &a0, void *scratch, cudaS
     TileOrder rows{0, 128, kKeys, nullptr}, keys{1, 128, kRows, nullptr};
     rows.out = reinterpret_cast<int2 *>(a.dks_heads + (size_t)a.total_k * a.H * a.Ds);
     keys.out = rows.out + tile_slots(a.total_q, a.num_seqs, 128);
-    const bool sorted = a.num_seqs > 1;           // two CTAs beside the others (blocks >= num_seqs >= 2)
+    const bool sorted = worth_order(a);           // two CTAs beside the others (blocks >= num_seqs >= 2)
     if (a.total_q > 0 || sorted) {
         e = launch_after(latent_stats_kernel, dim3(blocks, a.H + sorted), 256, 0, s, a, stats, rows, keys);
         if (e != cudaSuccess) return e;

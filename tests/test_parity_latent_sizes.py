@@ -114,10 +114,10 @@ def test_bf16_tiles_in_order(cuda_device, lq, lk, causal):
         assert all(torch.equal(g1[m], g[m][sq if m in ("dq", "dq_shared") else sk]) for m in NAMES)
 
 
-@pytest.mark.parametrize("count,H", [(600, 1), (1100, 1), (1100, 2)])
+@pytest.mark.parametrize("count,H", [(512, 1), (513, 1), (600, 2), (1100, 1), (1100, 2)])
 def test_bf16_more_sequences_than_threads(cuda_device, count, H):
     """More tiles than the ordering CTA has threads (512 and 256), and more sequences than it keeps offsets of (1024);
-    empty sequences among them, and some of several tiles."""
+    one head by places from 513 sequences on; empty sequences among them, and some of several tiles."""
     lq = [(7 * i) % 13 if i % 97 else 300 + i % 5 for i in range(count)]
     lk = [n + i % 3 if i % 11 else 0 for i, n in enumerate(lq)]
     x = packed(lq, lk, H, 64, 64, 64, BF16, seed=count + H)
