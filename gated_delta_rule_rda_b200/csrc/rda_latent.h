@@ -9,6 +9,8 @@
 
 namespace rda {
 
+constexpr int kSms = 148;      // streaming multiprocessors of a B200
+
 // Lets kernel K have `bytes` of dynamic shared memory, once per device (the
 // attribute belongs to the device's copy of the kernel).
 template <auto K> cudaError_t allow_smem(size_t bytes) {

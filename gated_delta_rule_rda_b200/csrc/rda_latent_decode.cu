@@ -64,7 +64,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kTok = 64;                 // tokens per tile
-constexpr int kCtas = 148;               // one CTA per SM
+constexpr int kCtas = kSms;              // one CTA per SM
 constexpr int kScan = 128;               // threads that sum up the lengths
 constexpr uint32_t kPair = 16384;        // 64 tokens x 128 latent columns; a slot is one or two of them
 constexpr uint32_t kBox = 8192;          // 64 tokens x 64 columns

@@ -441,10 +441,10 @@ __global__ void __launch_bounds__(256) latent_shared_sum_kernel(const float *par
 
 // Fewer tiles of 64 rows than SMs: smaller tiles; in the forward pass of 16, and the keys split until two CTAs per
 // SM have work (8 at most).
-bool few_tiles(int total, int H) { return (long)(total / kTile + 1) * H < 148; }
+bool few_tiles(int total, int H) { return (long)(total / kTile + 1) * H < kSms; }
 int forward_splits(int total_q, int total_k, int H) {
     if (!few_tiles(total_q, H)) return 1;
-    const long ctas = (long)(total_q / 16 + 1) * H, want = 296 / ctas, tiles = (total_k + kTile - 1) / kTile;
+    const long ctas = (long)(total_q / 16 + 1) * H, want = 2 * kSms / ctas, tiles = (total_k + kTile - 1) / kTile;
     return (int)std::max(1L, std::min({want, tiles, 8L}));
 }
 
@@ -471,7 +471,7 @@ template <typename T, int NDV> cudaError_t forward_nv(const LatentArgs &a, cudaS
     // 128 rows a CTA, unless 64 balance better: up to one and a half waves of them (16 heads of 1100 queries: 247 us
     // with 64 rows, 385 with 128; of 1500: 445 and 510; of 2000: 735 and 678).
     if (!few_tiles(a.total_q, a.H))
-        return (long)(a.total_q / 128 + 1) * a.H < 222 ? forward_ri<T, NDV, 4, 256>(a, 1, s) : forward_ri<T, NDV, 4, 512>(a, 1, s);
+        return (long)(a.total_q / 128 + 1) * a.H < kSms * 3 / 2 ? forward_ri<T, NDV, 4, 256>(a, 1, s) : forward_ri<T, NDV, 4, 512>(a, 1, s);
     return forward_ri<T, NDV, 1, 256>(a, forward_splits(a.total_q, a.total_k, a.H), s);
 }
 
@@ -703,7 +703,7 @@ int decode_rows(int rows) { return rows > 16 ? 32 : 16; }
 int decode_splits(int B, int rows) {
     const int tile = decode_rows(rows);
     const long units = (long)B * ((rows + tile - 1) / tile);
-    const long want = (296 + units - 1) / units;
+    const long want = (2 * kSms + units - 1) / units;
     return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
 }
 

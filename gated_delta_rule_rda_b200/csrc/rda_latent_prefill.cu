@@ -382,7 +382,7 @@ cudaError_t launch_latent_forward_tc(const LatentArgs &a0, void *scratch, cudaSt
     // Where the CTAs need more than one wave and sequences may differ, the order is worth a small kernel whose
     // launch and run mostly hide: 8 sequences of 0 to 2048 queries take 82.3 us by their places and 79.9 us in
     // order; a single wave, or one sequence, has nothing to gain.
-    const bool sorted = worth_order(a) && (long)slots * a.H > 148;
+    const bool sorted = worth_order(a) && (long)slots * a.H > kSms;
     if (sorted) {
         TileOrder o{0, kQ * kBM, kBN, static_cast<int2 *>(scratch)};
         if ((e = launch_after(latent_order_kernel, 1, 512, 0, s, a, o)) != cudaSuccess) return e;

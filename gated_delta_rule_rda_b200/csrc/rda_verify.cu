@@ -268,14 +268,14 @@ cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
     if (ns <= 2 * kMostCtas * kWarps) {
         // CTAs of a sequence: until every warp has one slice at most, or every SM two CTAs
         int ctas = 1;
-        while (ctas < kMostCtas && ctas * kWarps < ns && (long)a.B * ctas < 2 * 148) ctas *= 2;
+        while (ctas < kMostCtas && ctas * kWarps < ns && (long)a.B * ctas < 2 * kSms) ctas *= 2;
         return launch_clusters_after(vec ? verify_kernel<true> : verify_kernel<false>, ctas, dim3(ctas, a.B), kThreads, 0, s, a);
     }
     // At most 8 CTAs an SM, every warp with as many slices as the others.  80 registers let 3 of them run at once (4
     // without 128-bit loads), in two to three waves; a grid of 3 or 4 an SM is no faster, us on the device: 64 sequences
     // of 259,840 23.5 either way, of 200,003 23.2 against 21.8, 16 of 259,840 9.2 against 10.7, 250 of 140,000 40
     // against 51.
-    const int need = (ns + kWarps - 1) / kWarps, wave = (148 * 8 + a.B - 1) / a.B;
+    const int need = (ns + kWarps - 1) / kWarps, wave = (kSms * 8 + a.B - 1) / a.B;
     const int rounds = (need + wave - 1) / wave;
     const dim3 grid((need + rounds - 1) / rounds, a.B);
     const cudaError_t e = launch_after(vec ? verify_sums_kernel<true> : verify_sums_kernel<false>, grid, kThreads, 0, s, a);
