@@ -40,8 +40,9 @@
 // maximum, its relative error 2^-8 at most); sums and statistics are fp32.
 //
 // Measured (Dl + Ds = 512 + 64, 16 heads; this kernel, without the join):
-//   256 sequences of up to 4096 tokens, 16 rows     106 us, 5.8 TB/s (88% of a copy's rate)
-//   32 of up to 8192, 8 tokens: 128 rows, two CTAs   78 us; what bounds it is how long a
+//   256 sequences of up to 4096 tokens, 16 rows     106 to 109 us, 5.7 TB/s (87% of a copy's
+//               rate); a call, which joins the parts too, 111 on the device
+//   32 of up to 8192, 8 tokens: 128 rows, two CTAs   78 to 82 us; what bounds it is how long a
 //               tile stays in the ring, which holds two beside 64 rows of Q: 3,300 cycles a
 //               tile, of which the MMAs take 1,950
 // Copies by TMA took one box per page and chunk, ~200 cycles each whatever its size:
@@ -429,6 +430,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_decode_kernel(const 
     }
     constexpr uint32_t kCols = NT <= 16 ? 128 : NT <= 32 ? 256 : 512;      // 4 NT for O^T, 2 NT for S^T
 
+    // Ahead of the wait below: TMEM cannot run short between this kernel and one before it that still has to allocate
+    // its own, as their CTAs (74 KB of shared memory at least) do not fit on an SM beside one of this kernel's (200 KB).
     if (warp == 0) {
         tmem_alloc(&S.tmem, kCols);
         tmem_relinquish();

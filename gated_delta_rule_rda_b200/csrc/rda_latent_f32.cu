@@ -4,12 +4,14 @@
 //   s_ij = scale (q_i . k_j + q~_i . k~_j),  p = softmax_j s,  o_i = sum_j p_ij v_j
 //   ds_ij = p_ij (do_i . v_j - do_i . o_i),  dq = scale ds k,  dk = scale ds^T q,  dv = p^T do
 //
-// fp32 inputs are held to fp32 accuracy, which tensor-core operands of 16 or
-// 19 bits do not give, so these kernels run on FMAs: register tiles of 4 x 4
-// scores and 4 x (D / 16) outputs a thread, operands as fp32 rows in shared
-// memory (a row stride of D + 4 floats keeps the 128-bit reads of eight
-// consecutive rows on different banks).  Bound by the FMA pipes and the reads of
-// shared memory that feed them.
+// fp32 inputs are held to fp32 accuracy, which one product of 16- or 19-bit
+// tensor-core operands does not give.  Operands split in two or three terms would
+// (rda_decode_tokens does so), at three to six products each; these kernels are
+// the simpler form, on FMAs: register tiles of 4 x 4 scores and 4 x (D / 16)
+// outputs a thread, operands as fp32 rows in shared memory (a row stride of D + 4
+// floats keeps the 128-bit reads of eight consecutive rows on different banks).
+// Bound by the reads of shared memory that feed the FMAs, at a quarter to two
+// fifths of the FMA rate (74 TFLOP/s).
 //
 // Measured, 16 heads of 128 + 64 and 128, causal: T = 1100 in 247 us, T = 2000 in 678
 // us (25 and 30 TFLOP/s), gradients of T = 900 in 621 us (17); two heads, T = 256: 7.9

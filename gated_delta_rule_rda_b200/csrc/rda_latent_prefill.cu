@@ -30,8 +30,9 @@
 // Measured, 16 heads of 128 + 64 and 128, causal: T = 8192 in 285 us (1.2 PFLOP/s of
 // the visible pairs, 73% of what a library's plain product reaches; 335 us in a loop
 // under the power cap), T = 4096 in 80 us.  The two products of a step take 1,900
-// cycles of tensor pipe, a step 2,600: the scores read both operands from shared
-// memory, whose bandwidth the copies share.  A pair of CTAs that share the keys
+// cycles of tensor pipe (288 of them reread Q), a step 2,600: the rest is what the
+// chain of scores, softmax and values leaves exposed, 1,280 cycles of exponentials
+// in it.  A pair of CTAs that share the keys
 // (cta_group::2, half the reads) measured 389 us against 302 then: its barriers between CTAs cost more
 // than the reads.
 #include <cmath>

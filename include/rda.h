@@ -436,6 +436,10 @@ rda_status_t rda_prefill_chunked_noalloc(const void *q, const void *k, const voi
  * Preconditions, not checked: finite inputs within the sequences.  Sums, softmax
  * statistics and (for fp32) products are fp32; bf16 inputs run on the tensor cores,
  * with the probabilities rounded to bf16 for their product with v.
+ * A call repeated gives the same bits.  For bf16 a sequence's results are also the
+ * same bits whatever it is packed with; for fp32, and in rda_latent_decode, the
+ * keys are split by the size of the whole batch, and sums may differ in their last
+ * bits.
  */
 size_t rda_latent_prefill_workspace_bytes(int total_q, int total_k, int H, int Dk, int Ds, int Dv, int num_seqs);
 
