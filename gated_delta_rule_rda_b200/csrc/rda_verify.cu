@@ -272,7 +272,7 @@ cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t s) {
         return launch_clusters_after(vec ? verify_kernel<true> : verify_kernel<false>, ctas, dim3(ctas, a.B), kThreads, 0, s, a);
     }
     // At most 8 CTAs an SM, every warp with as many slices as the others.  80 registers let 3 of them run at once (4
-    // without 128-bit loads), in two to three waves; a grid of 3 or 4 an SM is no faster, us on the device: 64 sequences
+    // without 128-bit loads), in two to three waves; a grid of 3 or 4 an SM is no faster on the whole, us on the device: 64 sequences
     // of 259,840 23.5 either way, of 200,003 23.2 against 21.8, 16 of 259,840 9.2 against 10.7, 250 of 140,000 40
     // against 51.
     const int need = (ns + kWarps - 1) / kWarps, wave = (kSms * 8 + a.B - 1) / a.B;
